@@ -313,6 +313,107 @@ NVFP4_API nvfp4_status int8_linear(const void* x_bf16, int64_t M, int64_t K, con
                                    const float* sw, int64_t N, const void* bias_bf16,
                                    void* workspace, size_t ws_bytes, void* y_bf16, void* stream);
 
+/* ---- norm in front of a quantized linear ------------------------------------------ */
+/*
+ * What a transformer block does between two linears, in one pass over the rows
+ * (the pages' linears take the normed hidden states of a pre-norm block as x):
+ *     h = bf16(x + residual)                     (fp32 sum; h = x without a residual)
+ *     rstd = fp32(1 / sqrt(mean(h^2) + eps))     (the mean and the root in 64 bits)
+ *     n = bf16(fp32(fp32(h * rstd) * weight))
+ * and then the library's own encoding of n, bit for bit.  A row of zeros gives n = 0.
+ *   x            : in,  bf16 [rows, K]; K % 16 == 0, K <= 65536
+ *   residual     : in,  bf16 [rows, K] or NULL
+ *   weight       : in,  bf16 [K] or NULL (ones)
+ *   eps          : host value, finite and > 0
+ *   residual_out : out, bf16 [rows, K] = h, or NULL; needs a residual; may equal x or
+ *                  residual (in place)
+ *   norm_out     : out, bf16 [rows, K] = n, or NULL; may not overlap the inputs
+ */
+
+/*
+ * int8_rmsnorm_quantize -- the codes of int8_quantize_rows(n).
+ *   q : out, int8 [rows, K];  scale : out, fp32 [rows]
+ * Errors: INVALID_ARG (null x, q or scale; rows < 0; eps; residual_out without residual),
+ * SHAPE (K), ALIGN (bf16 tensors and q 16-byte, scale 4-byte), DEVICE, CUDA.
+ */
+NVFP4_API nvfp4_status int8_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16,
+                                             const void* weight_bf16, double eps, int64_t rows,
+                                             int64_t K, int8_t* q, float* scale,
+                                             void* residual_out_bf16, void* norm_out_bf16,
+                                             void* stream);
+
+/*
+ * nvfp4_rmsnorm_quantize -- the codes of nvfp4_quantize(n, rotate_group 0, gsf_in = gsf):
+ * a static global scale, no rotation (a dynamic scale or a rotation takes norm_out and
+ * nvfp4_quantize).
+ *   gsf              : in,  device fp32 scalar, the static global scale
+ *   packed, sf       : out, as nvfp4_quantize (sf with its padding written as 0)
+ *   gsf_w, alpha_out : as nvfp4_quantize: both NULL or both given
+ * Errors: as int8_rmsnorm_quantize; ALIGN also for packed, sf (16-byte) and the scalars
+ * (4-byte).
+ */
+NVFP4_API nvfp4_status nvfp4_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16,
+                                              const void* weight_bf16, double eps, int64_t rows,
+                                              int64_t K, const float* gsf, uint8_t* packed,
+                                              uint8_t* sf, const float* gsf_w, float* alpha_out,
+                                              void* residual_out_bf16, void* norm_out_bf16,
+                                              void* stream);
+
+/* ---- products with an activation and a residual in their epilogue --------------------- */
+/* Activation of a *_act call: one of the first five, and NVFP4_ACT_GATED added to it for
+ * the gated form. */
+#define NVFP4_ACT_NONE 0
+#define NVFP4_ACT_RELU 1
+#define NVFP4_ACT_GELU 2        /* v * Phi(v), by the error function */
+#define NVFP4_ACT_GELU_TANH 3   /* v / 2 * (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+#define NVFP4_ACT_SILU 4        /* v / (1 + exp(-v)) */
+#define NVFP4_ACT_GATED 16
+
+/*
+ * nvfp4_gemm_act, int8_gemm_act -- nvfp4_gemm (nvfp4_gemm_prepared with sfb_prepared = 1)
+ * and int8_gemm with more in the epilogue:
+ *     v = fp32(alpha * acc) + bias[n]              (int8: (fp32(acc) * sa[m]) * sb[n] + bias)
+ *     u[m, n] = act(v[m, n])                       plain: n_out = N columns
+ *     u[m, j] = act(v[m, 2j]) * v[m, 2j + 1]       gated: n_out = N / 2 columns
+ *     y[m, j] = bf16(u[m, j] + residual[m, j])
+ * in fp32 with the one rounding at the end.  The activations are within 5e-7 * max(|v|, 1)
+ * of their 64-bit values before that rounding.
+ *   activation    : NVFP4_ACT_*; gated: the weight's rows 2j and 2j + 1 hold the gate's and
+ *                   the up projection's row j (bias likewise), N even
+ *   residual_bf16 : in,  bf16 [M, n_out] or NULL; may equal y (in place), otherwise may not
+ *                   overlap it
+ *   y_bf16        : out, bf16 [M, n_out]
+ * int8: K <= 131040, so that every sum of code products is exact in 32 bits.
+ * Errors: INVALID_ARG (also an unknown activation, sfb_prepared not 0 or 1), SHAPE (also
+ * gated with N odd), ALIGN (also residual 16-byte), DEVICE, CUDA.
+ */
+NVFP4_API nvfp4_status nvfp4_gemm_act(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
+                                      const uint8_t* sfb, int sfb_prepared, const float* alpha,
+                                      const void* bias_bf16, int activation,
+                                      const void* residual_bf16, void* y_bf16, int64_t M,
+                                      int64_t N, int64_t K, void* stream);
+NVFP4_API nvfp4_status int8_gemm_act(const int8_t* a, const float* sa, const int8_t* b,
+                                     const float* sb, const void* bias_bf16, int activation,
+                                     const void* residual_bf16, void* y_bf16, int64_t M, int64_t N,
+                                     int64_t K, void* stream);
+
+/*
+ * nvfp4_linear_act, int8_linear_act -- nvfp4_linear (nvfp4_linear_prepared with
+ * w_sf_prepared = 1) and int8_linear ending in the same epilogue; arguments, workspace and
+ * errors otherwise as theirs.
+ */
+NVFP4_API nvfp4_status nvfp4_linear_act(const void* x_bf16, int64_t M, int64_t K,
+                                        const uint8_t* w_packed, const uint8_t* w_sf,
+                                        int w_sf_prepared, const float* gsf_w, int64_t N,
+                                        const void* bias_bf16, const float* gsf_x,
+                                        int rotate_group, int activation,
+                                        const void* residual_bf16, void* workspace,
+                                        size_t ws_bytes, void* y_bf16, void* stream);
+NVFP4_API nvfp4_status int8_linear_act(const void* x_bf16, int64_t M, int64_t K, const int8_t* wq,
+                                       const float* sw, int64_t N, const void* bias_bf16,
+                                       int activation, const void* residual_bf16, void* workspace,
+                                       size_t ws_bytes, void* y_bf16, void* stream);
+
 /* Size of the library's own fixed device scratch used by
  * nvfp4_linear_fixed_scratch: 8 MiB. */
 #define NVFP4_FIXED_SCRATCH_BYTES ((size_t)8 << 20)

@@ -25,6 +25,7 @@ OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_ALIGN, ERR_WORKSPACE, ERR_DEVICE, ERR_CUDA, 
 
 # name -> (restype, argtypes); the full exported surface of include/nvfp4.h
 _vp, _i64, _sz, _int, _u32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint32
+_f64 = ctypes.c_double
 SIGNATURES = {
     "nvfp4_status_string": (ctypes.c_char_p, [_int]),
     "nvfp4_abi_version": (_int, []),
@@ -52,6 +53,16 @@ SIGNATURES = {
                                      _sz, _vp, _vp]),
     "nvfp4_linear_fixed_scratch": (_int, [_vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _int,
                                           _vp, _vp]),
+    "int8_rmsnorm_quantize": (_int, [_vp, _vp, _vp, _f64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "nvfp4_rmsnorm_quantize": (_int, [_vp, _vp, _vp, _f64, _i64, _i64, _vp, _vp, _vp, _vp, _vp,
+                                      _vp, _vp, _vp]),
+    "nvfp4_gemm_act": (_int, [_vp, _vp, _vp, _vp, _int, _vp, _vp, _int, _vp, _vp, _i64, _i64,
+                              _i64, _vp]),
+    "int8_gemm_act": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _i64, _i64, _i64, _vp]),
+    "nvfp4_linear_act": (_int, [_vp, _i64, _i64, _vp, _vp, _int, _vp, _i64, _vp, _vp, _int, _int,
+                                _vp, _vp, _sz, _vp, _vp]),
+    "int8_linear_act": (_int, [_vp, _i64, _i64, _vp, _vp, _i64, _vp, _int, _vp, _vp, _sz, _vp,
+                               _vp]),
     "nvfp4_last_device_status": (_int, [_vp, ctypes.POINTER(_int)]),
     "nvfp4_debug_cvt_sweep": (_int, [_u32, _i64, _vp, _vp, _vp, _vp]),
     "nvfp4_debug_wait_timeout": (_int, [_i64, _vp]),
@@ -114,6 +125,43 @@ def _scalar(t, device, name):
     if t.dtype != torch.float32 or t.numel() != 1 or not t.is_cuda:
         raise TypeError(f"{name} must be a one-element CUDA float32 tensor")
     return t
+
+
+def _need(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype,
+          device: torch.device) -> int | None:
+    """The address of a tensor argument that has to be exactly this (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.device != device:
+        raise TypeError(f"{name} must be a {dtype} tensor on {device}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _need_bytes(t: torch.Tensor, name: str, least: int, device: torch.device) -> int:
+    """The address of a packed uint8 buffer of at least `least` bytes."""
+    if t.dtype is not torch.uint8 or t.device != device:
+        raise TypeError(f"{name} must be a torch.uint8 tensor on {device}")
+    if t.numel() < least or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and hold at least {least} bytes")
+    return t.data_ptr()
+
+
+def _here(t: torch.Tensor, name: str) -> torch.device:
+    """The device of a call's first tensor, which has to be the current one: the library
+    launches on the current device."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return t.device
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    lo = max(a.data_ptr(), b.data_ptr())
+    return lo < min(a.data_ptr() + a.numel() * a.element_size(),
+                    b.data_ptr() + b.numel() * b.element_size())
 
 
 # ---------------------------------------------------------------------------
@@ -316,6 +364,210 @@ def int8_linear(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
     _check("int8_linear", lib().int8_linear(_ptr(x), M, K, _ptr(wq), _ptr(sw), N, _ptr(bias),
                                             _ptr(workspace), workspace.numel(), _ptr(y),
                                             _stream(stream)))
+    return y
+
+
+# ---------------------------------------------------------------------------
+# norm in front of a quantized linear
+# ---------------------------------------------------------------------------
+
+def _norm_inputs(x, weight, residual, residual_out, norm_out):
+    dev = _here(x, "x")
+    _bf16_2d(x, "x")
+    shape = x.shape
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    for t, name in ((residual, "residual"), (x, "x")):
+        if (residual_out is not None and t.data_ptr() != residual_out.data_ptr()
+                and _overlap(t, residual_out)):
+            raise ValueError(f"residual_out must be {name} itself or not overlap it")
+    if norm_out is not None and any(t is not None and _overlap(norm_out, t)
+                                    for t in (x, residual, residual_out)):
+        raise ValueError("norm_out must not overlap the other tensors")
+    return dev, residual_out, (
+        x.data_ptr(), _need(residual, "residual", shape, torch.bfloat16, dev),
+        _need(weight, "weight", shape[1:], torch.bfloat16, dev)), (
+        _need(residual_out, "residual_out", shape, torch.bfloat16, dev),
+        _need(norm_out, "norm_out", shape, torch.bfloat16, dev))
+
+
+def int8_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None, eps: float,
+                          residual: torch.Tensor | None = None, out: tuple | None = None,
+                          residual_out: torch.Tensor | None = None,
+                          norm_out: torch.Tensor | None = None, stream=None):
+    """h = bf16(x + residual); n = bf16(h * rstd * weight); the per-row int8 codes of n.
+
+    Returns (codes int8 [rows, K], scales fp32 [rows], h): h is residual_out, allocated when
+    it is not given, or None without a residual.  residual_out may be x or residual itself.
+    norm_out, when given, receives n."""
+    dev, residual_out, ins, outs = _norm_inputs(x, weight, residual, residual_out, norm_out)
+    R, K = x.shape
+    if out is None:
+        out = (torch.empty(R, K, dtype=torch.int8, device=dev),
+               torch.empty(R, dtype=torch.float32, device=dev))
+    q, s = out
+    args = (
+        *ins, eps, R, K, _need(q, "codes", x.shape, torch.int8, dev),
+        _need(s, "scales", x.shape[:1], torch.float32, dev), *outs, _stream(stream))
+    if R:   # an empty tensor has no address
+        _check("int8_rmsnorm_quantize", lib().int8_rmsnorm_quantize(*args))
+    return q, s, residual_out
+
+
+def nvfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None, gsf: torch.Tensor,
+                           eps: float, residual: torch.Tensor | None = None,
+                           out: tuple | None = None, residual_out: torch.Tensor | None = None,
+                           norm_out: torch.Tensor | None = None,
+                           gsf_w: torch.Tensor | None = None,
+                           alpha_out: torch.Tensor | None = None, stream=None):
+    """The same norm with NVFP4 codes under the static global scale gsf.
+
+    Returns (packed uint8 [rows, K/2], scales uint8 [scale_bytes], h).  With gsf_w and
+    alpha_out the kernel also writes alpha = 1/(gsf * gsf_w)."""
+    dev, residual_out, ins, outs = _norm_inputs(x, weight, residual, residual_out, norm_out)
+    R, K = x.shape
+    one = (1,)
+    if out is None:
+        out = (torch.empty(R, K // 2, dtype=torch.uint8, device=dev),
+               torch.empty(nvfp4_scale_bytes(R, K), dtype=torch.uint8, device=dev))
+    packed, sf = out
+    args = (
+        *ins, eps, R, K, _need(gsf, "gsf", one, torch.float32, dev),
+        _need(packed, "packed", (R, K // 2), torch.uint8, dev),
+        _need_bytes(sf, "scales", lib().nvfp4_scale_bytes(R, K), dev),
+        _need(gsf_w, "gsf_w", one, torch.float32, dev),
+        _need(alpha_out, "alpha_out", one, torch.float32, dev), *outs, _stream(stream))
+    if R:   # an empty tensor has no address
+        _check("nvfp4_rmsnorm_quantize", lib().nvfp4_rmsnorm_quantize(*args))
+    return packed, sf, residual_out
+
+
+# ---------------------------------------------------------------------------
+# products with an activation and a residual in their epilogue
+# ---------------------------------------------------------------------------
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+ACT_GATED = 16
+
+
+def interleave_gate_up(gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
+    """The rows (of weights) or values (of biases) of a gated pair in the order the gated
+    epilogues take them: gate 0, up 0, gate 1, up 1, ..."""
+    if gate.shape != up.shape:
+        raise ValueError("gate and up must have the same shape")
+    return torch.stack((gate, up), dim=1).reshape(2 * gate.shape[0], *gate.shape[1:])
+
+
+def _epilogue(activation, gated, residual, bias, out, M, N, dev):
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
+    if gated and N % 2:
+        raise ValueError("a gated product has an even number of weight rows")
+    shape = (M, N // 2 if gated else N)
+    y = torch.empty(shape, dtype=torch.bfloat16, device=dev) if out is None else out
+    y_ptr = _need(y, "out", shape, torch.bfloat16, dev)
+    r_ptr = _need(residual, "residual", shape, torch.bfloat16, dev)
+    if r_ptr is not None and r_ptr != y_ptr and _overlap(residual, y):
+        raise ValueError("residual must be out itself or not overlap it")
+    return (y, y_ptr, r_ptr, _need(bias, "bias", (N,), torch.bfloat16, dev),
+            ACTIVATIONS[activation] + (ACT_GATED if gated else 0))
+
+
+def nvfp4_gemm_act(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: torch.Tensor,
+                   alpha: torch.Tensor, bias: torch.Tensor | None, M: int, N: int, K: int,
+                   activation: str = "none", gated: bool = False,
+                   residual: torch.Tensor | None = None, prepared: bool = False,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y bf16 = bf16(act(alpha * deq(a) deq(b)^T + bias) + residual); gated: over the column
+    pairs (gate, up) of a weight in the order of interleave_gate_up, y [M, N/2].  With
+    prepared=True, sfb is the output of prepare_weight_scales.  residual may be out."""
+    dev = _here(a, "a")
+    L = lib()
+    y, y_ptr, r_ptr, b_ptr, act = _epilogue(activation, gated, residual, bias, out, M, N, dev)
+    sfb_bytes = L.nvfp4_prepared_scale_bytes(N, K) if prepared else L.nvfp4_scale_bytes(N, K)
+    args = (
+        _need_bytes(a, "a", M * K // 2, dev), _need_bytes(sfa, "sfa", L.nvfp4_scale_bytes(M, K), dev),
+        _need_bytes(b, "b", N * K // 2, dev), _need_bytes(sfb, "sfb", sfb_bytes, dev),
+        1 if prepared else 0, _need(alpha, "alpha", (1,), torch.float32, dev), b_ptr, act, r_ptr,
+        y_ptr, M, N, K, _stream(stream))
+    if M and N:   # an empty tensor has no address
+        _check("nvfp4_gemm_act", L.nvfp4_gemm_act(*args))
+    return y
+
+
+def int8_gemm_act(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor,
+                  bias: torch.Tensor | None = None, activation: str = "none", gated: bool = False,
+                  residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """y bf16 = bf16(act((fp32(a b^T) * sa[m]) * sb[n] + bias) + residual); gated as in
+    nvfp4_gemm_act.  residual may be out."""
+    dev = _here(a, "a")
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise ValueError("a [M, K] and b [N, K] must be 2-D with the same K")
+    M, K = a.shape
+    N = b.shape[0]
+    y, y_ptr, r_ptr, b_ptr, act = _epilogue(activation, gated, residual, bias, out, M, N, dev)
+    args = (
+        _need(a, "a", a.shape, torch.int8, dev), _need(sa, "sa", (M,), torch.float32, dev),
+        _need(b, "b", b.shape, torch.int8, dev), _need(sb, "sb", (N,), torch.float32, dev),
+        b_ptr, act, r_ptr, y_ptr, M, N, K, _stream(stream))
+    if M and N:   # an empty tensor has no address
+        _check("int8_gemm_act", lib().int8_gemm_act(*args))
+    return y
+
+
+def nvfp4_linear_act(x: torch.Tensor, w_packed: torch.Tensor, w_sf: torch.Tensor,
+                     gsf_w: torch.Tensor, N: int, bias: torch.Tensor | None = None,
+                     activation: str = "none", gated: bool = False,
+                     residual: torch.Tensor | None = None,
+                     gsf_x: torch.Tensor | None = None, rotate_group: int = 0,
+                     prepared: bool = False, workspace: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """nvfp4_linear ending in the epilogue of nvfp4_gemm_act."""
+    dev = _here(x, "x")
+    _bf16_2d(x, "x")
+    M, K = x.shape
+    L = lib()
+    y, y_ptr, r_ptr, b_ptr, act = _epilogue(activation, gated, residual, bias, out, M, N, dev)
+    if workspace is None:
+        workspace = torch.empty(nvfp4_linear_workspace_bytes(M, K), dtype=torch.uint8, device=dev)
+    ws_ptr = _need_bytes(workspace, "workspace", 0, dev)
+    sf_bytes = L.nvfp4_prepared_scale_bytes(N, K) if prepared else L.nvfp4_scale_bytes(N, K)
+    args = (
+        x.data_ptr(), M, K, _need_bytes(w_packed, "w_packed", N * K // 2, dev),
+        _need_bytes(w_sf, "w_sf", sf_bytes, dev), 1 if prepared else 0,
+        _need(gsf_w, "gsf_w", (1,), torch.float32, dev), N, b_ptr,
+        _need(gsf_x, "gsf_x", (1,), torch.float32, dev), int(rotate_group), act, r_ptr, ws_ptr,
+        workspace.numel(), y_ptr, _stream(stream))
+    if M and N:   # an empty tensor has no address
+        _check("nvfp4_linear_act", L.nvfp4_linear_act(*args))
+    return y
+
+
+def int8_linear_act(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
+                    bias: torch.Tensor | None = None, activation: str = "none",
+                    gated: bool = False, residual: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """int8_linear ending in the epilogue of int8_gemm_act."""
+    dev = _here(x, "x")
+    _bf16_2d(x, "x")
+    M, K = x.shape
+    N = wq.shape[0]
+    L = lib()
+    y, y_ptr, r_ptr, b_ptr, act = _epilogue(activation, gated, residual, bias, out, M, N, dev)
+    if workspace is None:
+        workspace = torch.empty(max(int(L.int8_linear_workspace_bytes(M, K)), 1),
+                                dtype=torch.uint8, device=dev)
+    ws_ptr = _need_bytes(workspace, "workspace", 0, dev)
+    args = (
+        x.data_ptr(), M, K, _need(wq, "wq", (N, K), torch.int8, dev),
+        _need(sw, "sw", (N,), torch.float32, dev), N, b_ptr, act, r_ptr, ws_ptr,
+        workspace.numel(), y_ptr, _stream(stream))
+    if M and N:   # an empty tensor has no address
+        _check("int8_linear_act", L.int8_linear_act(*args))
     return y
 
 

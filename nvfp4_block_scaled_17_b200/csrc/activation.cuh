@@ -1,0 +1,130 @@
+// activation.cuh -- the activations of the GEMM epilogues, in fp32.
+//
+//   relu       max(v, 0)
+//   gelu       v * Phi(v), Phi the normal distribution function
+//   gelu_tanh  v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3)))
+//   silu       v / (1 + exp(-v))
+// A gated epilogue takes column pairs: u[j] = act(v[2j]) * v[2j + 1].
+//
+// Two special-function operations per value (one exponential, one reciprocal), the rest on
+// the FMA pipe.  Errors against 64-bit values, before the one rounding to bf16 (2^-9
+// relative): below 5e-7 max(|v|, 1).
+#pragma once
+
+#include "common.cuh"
+
+namespace nvfp4 {
+
+__device__ __forceinline__ float ex2_approx(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// v / (1 + 2^t).  t is held below 126, so the sum stays finite and its reciprocal normal;
+// there the quotient is v 2^-126, zero to every bf16 that it can be added to.
+__device__ __forceinline__ float over_one_plus_exp2(float v, float t) {
+    return v * rcp_approx(1.0f + ex2_approx(fminf(t, 126.0f)));
+}
+
+__device__ __forceinline__ float act_silu(float v) { return over_one_plus_exp2(v, -kLog2e * v); }
+
+// (1 + tanh(z)) / 2 = 1 / (1 + exp(-2 z))
+__device__ __forceinline__ float act_gelu_tanh(float v) {
+    constexpr float c = -2.0f * 0.79788456080286535588f * kLog2e;
+    return over_one_plus_exp2(v, v * fmaf(c * 0.044715f, v * v, c));
+}
+
+// v Phi(v) = max(v, 0) - |v| Q(|v|), Q(z) = erfc(z / sqrt 2) / 2 by the rational form of
+// Hastings ("Approximations for Digital Computers", sheet 45; also Abramowitz and Stegun
+// 7.1.26, |error of erf| <= 1.5e-7): erfc(y) = t (a1 + t (a2 + ...)) exp(-y^2),
+// t = 1 / (1 + p y).
+__device__ __forceinline__ float act_gelu(float v) {
+    const float z = fabsf(v);
+    const float t = rcp_approx(fmaf(0.3275911f * 0.70710678118654752440f, z, 1.0f));
+    float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+    q = fmaf(t, q, 0.5f * 1.421413741f);
+    q = fmaf(t, q, 0.5f * -0.284496736f);
+    q = fmaf(t, q, 0.5f * 0.254829592f);
+    const float e = ex2_approx((-0.5f * kLog2e) * z * z);
+    return fmaf(-z * (t * q), e, fmaxf(v, 0.0f));
+}
+
+// act over the values of v that it applies to: all n, or (gated) the even ones, whose odd
+// neighbour is then multiplied in (the result stays at the even places).
+template <int N>
+__device__ __forceinline__ void apply_activation(float (&v)[N], int act, bool gated) {
+    const int base = act & ~NVFP4_ACT_GATED;
+    auto each = [&](auto f) {
+        if (gated) {
+#pragma unroll
+            for (int j = 0; j < N; j += 2) v[j] = f(v[j]) * v[j + 1];
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = f(v[j]);
+        }
+    };
+    switch (base) {
+        case NVFP4_ACT_RELU: each([](float x) { return fmaxf(x, 0.0f); }); break;
+        case NVFP4_ACT_GELU: each([](float x) { return act_gelu(x); }); break;
+        case NVFP4_ACT_GELU_TANH: each([](float x) { return act_gelu_tanh(x); }); break;
+        case NVFP4_ACT_SILU: each([](float x) { return act_silu(x); }); break;
+        default:
+            if (gated) each([](float x) { return x; });
+            break;
+    }
+}
+
+// Four consecutive columns (n % 4 == 0) of an output row, from the reduction phases of the
+// split-K builds: activation, residual, one rounding, store.  n_out: columns of y.
+__device__ __forceinline__ void finish_granule(float (&v)[4], int act, bool gated,
+                                               const uint16_t* residual, uint16_t* y, int64_t row,
+                                               int n, int n_out) {
+    apply_activation(v, act, gated);
+    if (gated) {
+        const int col = n >> 1;
+        const int64_t at = row * n_out + col;
+        float u[2] = {v[0], v[2]};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (residual && col + j < n_out)
+                u[j] = __fadd_rn(u[j], __uint_as_float((uint32_t)residual[at + j] << 16));
+        const uint32_t w = bf16x2_rn(u[0], u[1]);
+        if ((n_out & 1) == 0) {
+            *reinterpret_cast<uint32_t*>(y + at) = w;
+        } else {
+            y[at] = (uint16_t)w;
+            if (col + 1 < n_out) y[at + 1] = (uint16_t)(w >> 16);
+        }
+        return;
+    }
+    const int64_t at = row * n_out + n;
+    if ((n_out & 3) == 0) {
+        if (residual) {
+            const uint2 r = *reinterpret_cast<const uint2*>(residual + at);
+            v[0] = __fadd_rn(v[0], bf16lo(r.x));
+            v[1] = __fadd_rn(v[1], bf16hi(r.x));
+            v[2] = __fadd_rn(v[2], bf16lo(r.y));
+            v[3] = __fadd_rn(v[3], bf16hi(r.y));
+        }
+        *reinterpret_cast<uint2*>(y + at) = make_uint2(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]));
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (n + j < n_out) {
+            if (residual)
+                v[j] = __fadd_rn(v[j], __uint_as_float((uint32_t)residual[at + j] << 16));
+            y[at + j] = (uint16_t)bf16x2_rn(v[j], 0.0f);
+        }
+}
+
+}  // namespace nvfp4

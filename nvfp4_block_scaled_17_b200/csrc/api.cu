@@ -26,6 +26,16 @@ std::mutex g_mu;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+bool valid_activation(int act) {
+    const int base = act & ~NVFP4_ACT_GATED;
+    return base >= NVFP4_ACT_NONE && base <= NVFP4_ACT_SILU;
+}
+
+// |acc| <= 128 * 128 * K stays below 2^31 for K up to here (a multiple of 32).
+constexpr int64_t kInt8MaxK = 131040;
+
+bool gated(int act) { return (act & NVFP4_ACT_GATED) != 0; }
+
 bool valid_group(int g) { return g == 0 || g == 16 || g == 32 || g == 64 || g == 128; }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -422,6 +432,160 @@ nvfp4_status nvfp4_linear_fixed_scratch(const void* x, int64_t M, int64_t K,
                          s);
     if (st != NVFP4_OK) return st;
     return launch_gemm(xp, xsf, w_packed, w_sf, &scalars[1], bias, y, M, N, K, s, true);
+}
+
+nvfp4_status nvfp4_gemm_act(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
+                            const uint8_t* sfb, int sfb_prepared, const float* alpha,
+                            const void* bias, int activation, const void* residual, void* y,
+                            int64_t M, int64_t N, int64_t K, void* stream) {
+    if (!a || !sfa || !b || !sfb || !alpha || !y || M < 0 || N < 0 ||
+        (sfb_prepared != 0 && sfb_prepared != 1) || !valid_activation(activation))
+        return NVFP4_ERR_INVALID_ARG;
+    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
+    if (K <= 0 || K % 64 || K >= (int64_t(1) << 31) || (gated(activation) && N % 2))
+        return NVFP4_ERR_SHAPE;
+    if (!aligned(a, 16) || !aligned(sfa, 16) || !aligned(b, 16) || !aligned(sfb, 16) ||
+        !aligned(y, 16) || !aligned(alpha, 4) || (bias && !aligned(bias, 16)) ||
+        (residual && !aligned(residual, 16)))
+        return NVFP4_ERR_ALIGN;
+    DeviceInfo dev;
+    nvfp4_status st = device_info(&dev);
+    if (st != NVFP4_OK) return st;
+    if (M == 0 || N == 0) return NVFP4_OK;
+    return launch_gemm_act(a, sfa, b, sfb, sfb_prepared != 0, alpha, bias, {activation, residual},
+                           y, M, N, K, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_linear_act(const void* x, int64_t M, int64_t K, const uint8_t* w_packed,
+                              const uint8_t* w_sf, int w_sf_prepared, const float* gsf_w,
+                              int64_t N, const void* bias, const float* gsf_x, int group,
+                              int activation, const void* residual, void* workspace,
+                              size_t ws_bytes, void* y, void* stream) {
+    if (!x || !w_packed || !w_sf || !gsf_w || !y || M < 0 || N < 0 || !valid_group(group) ||
+        (w_sf_prepared != 0 && w_sf_prepared != 1) || !valid_activation(activation))
+        return NVFP4_ERR_INVALID_ARG;
+    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
+    if (K <= 0 || K % 64 || (group && K % group) || K >= (int64_t(1) << 31) ||
+        (gated(activation) && N % 2))
+        return NVFP4_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(w_packed, 16) || !aligned(w_sf, 16) || !aligned(y, 16) ||
+        !aligned(gsf_w, 4) || (gsf_x && !aligned(gsf_x, 4)) || (bias && !aligned(bias, 16)) ||
+        (residual && !aligned(residual, 16)))
+        return NVFP4_ERR_ALIGN;
+    const LinearWs ws = linear_ws(M, K);
+    if (!workspace || ws_bytes < ws.total) return NVFP4_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return NVFP4_ERR_ALIGN;
+    DeviceInfo dev;
+    nvfp4_status st = device_info(&dev);
+    if (st != NVFP4_OK) return st;
+    if (M == 0 || N == 0) return NVFP4_OK;
+
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    uint8_t* xp = base + ws.packed;
+    uint8_t* xsf = base + ws.sf;
+    float* scalars = reinterpret_cast<float*>(base + ws.scalars);
+    float* partials = reinterpret_cast<float*>(base + ws.partials);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = launch_quantize(x, M, K, group, gsf_x, &scalars[0], xp, xsf, partials, gsf_w, &scalars[1],
+                         s);
+    if (st != NVFP4_OK) return st;
+    return launch_gemm_act(xp, xsf, w_packed, w_sf, w_sf_prepared != 0, &scalars[1], bias,
+                           {activation, residual}, y, M, N, K, s, true);
+}
+
+nvfp4_status int8_gemm_act(const int8_t* a, const float* sa, const int8_t* b, const float* sb,
+                           const void* bias, int activation, const void* residual, void* y,
+                           int64_t M, int64_t N, int64_t K, void* stream) {
+    if (!a || !sa || !b || !sb || !y || M < 0 || N < 0 || !valid_activation(activation))
+        return NVFP4_ERR_INVALID_ARG;
+    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
+    if (K <= 0 || K % 32 || K > kInt8MaxK || (gated(activation) && N % 2)) return NVFP4_ERR_SHAPE;
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16) || !aligned(sa, 16) ||
+        !aligned(sb, 16) || (bias && !aligned(bias, 16)) || (residual && !aligned(residual, 16)))
+        return NVFP4_ERR_ALIGN;
+    DeviceInfo dev;
+    nvfp4_status st = device_info(&dev);
+    if (st != NVFP4_OK) return st;
+    if (M == 0 || N == 0) return NVFP4_OK;
+    return launch_int8_gemm_act(a, sa, b, sb, bias, {activation, residual}, y, M, N, K,
+                                static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status int8_linear_act(const void* x, int64_t M, int64_t K, const int8_t* wq,
+                             const float* sw, int64_t N, const void* bias, int activation,
+                             const void* residual, void* workspace, size_t ws_bytes, void* y,
+                             void* stream) {
+    if (!x || !wq || !sw || !y || M < 0 || N < 0 || !valid_activation(activation))
+        return NVFP4_ERR_INVALID_ARG;
+    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
+    if (K <= 0 || K % 32 || K > kInt8MaxK || (gated(activation) && N % 2)) return NVFP4_ERR_SHAPE;
+    if (!aligned(x, 16) || !aligned(wq, 16) || !aligned(sw, 16) || !aligned(y, 16) ||
+        (bias && !aligned(bias, 16)) || (residual && !aligned(residual, 16)))
+        return NVFP4_ERR_ALIGN;
+    const size_t need = int8_linear_workspace_bytes(M, K);
+    if (!workspace || ws_bytes < need) return NVFP4_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return NVFP4_ERR_ALIGN;
+    DeviceInfo dev;
+    nvfp4_status st = device_info(&dev);
+    if (st != NVFP4_OK) return st;
+    if (M == 0 || N == 0) return NVFP4_OK;
+    int8_t* xq = static_cast<int8_t*>(workspace);
+    float* sx = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                         align256((size_t)M * (size_t)K));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = launch_int8_quantize_rows(x, M, K, xq, sx, s);
+    if (st != NVFP4_OK) return st;
+    return launch_int8_gemm_act(xq, sx, wq, sw, bias, {activation, residual}, y, M, N, K, s);
+}
+
+// The arguments that both norm entry points share.
+static nvfp4_status check_norm(const NormInputs& in) {
+    if (!in.x || in.rows < 0 || !(in.eps > 0.0) || !std::isfinite(in.eps) ||
+        (in.residual_out && !in.residual))
+        return NVFP4_ERR_INVALID_ARG;
+    if (in.K <= 0 || in.K % 16 || in.K > kNormMaxK) return NVFP4_ERR_SHAPE;
+    if (!aligned(in.x, 16) || (in.residual && !aligned(in.residual, 16)) ||
+        (in.weight && !aligned(in.weight, 16)) ||
+        (in.residual_out && !aligned(in.residual_out, 16)) ||
+        (in.norm_out && !aligned(in.norm_out, 16)))
+        return NVFP4_ERR_ALIGN;
+    return NVFP4_OK;
+}
+
+nvfp4_status int8_rmsnorm_quantize(const void* x, const void* residual, const void* weight,
+                                   double eps, int64_t rows, int64_t K, int8_t* q, float* scale,
+                                   void* residual_out, void* norm_out, void* stream) {
+    const NormInputs in{x, residual, weight, eps, rows, K, residual_out, norm_out};
+    if (!q || !scale) return NVFP4_ERR_INVALID_ARG;
+    nvfp4_status st = check_norm(in);
+    if (st != NVFP4_OK) return st;
+    if (!aligned(q, 16) || !aligned(scale, 4)) return NVFP4_ERR_ALIGN;
+    DeviceInfo dev;
+    st = device_info(&dev);
+    if (st != NVFP4_OK) return st;
+    if (rows == 0) return NVFP4_OK;
+    return launch_int8_norm(in, q, scale, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_rmsnorm_quantize(const void* x, const void* residual, const void* weight,
+                                    double eps, int64_t rows, int64_t K, const float* gsf,
+                                    uint8_t* packed, uint8_t* sf, const float* gsf_w,
+                                    float* alpha_out, void* residual_out, void* norm_out,
+                                    void* stream) {
+    const NormInputs in{x, residual, weight, eps, rows, K, residual_out, norm_out};
+    if (!gsf || !packed || !sf || (gsf_w == nullptr) != (alpha_out == nullptr))
+        return NVFP4_ERR_INVALID_ARG;
+    nvfp4_status st = check_norm(in);
+    if (st != NVFP4_OK) return st;
+    if (!aligned(packed, 16) || !aligned(sf, 16) || !aligned(gsf, 4) ||
+        (gsf_w && !aligned(gsf_w, 4)) || (alpha_out && !aligned(alpha_out, 4)))
+        return NVFP4_ERR_ALIGN;
+    DeviceInfo dev;
+    st = device_info(&dev);
+    if (st != NVFP4_OK) return st;
+    if (rows == 0) return NVFP4_OK;
+    return launch_nvfp4_norm(in, gsf, packed, sf, gsf_w, alpha_out,
+                             static_cast<cudaStream_t>(stream));
 }
 
 nvfp4_status nvfp4_debug_gemm_f32(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,

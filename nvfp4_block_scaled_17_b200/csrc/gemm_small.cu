@@ -37,6 +37,7 @@
 // copies and MMAs, frees tensor memory and returns.  No load uses cluster multicast.
 #include <atomic>
 
+#include "activation.cuh"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -79,6 +80,14 @@ struct SmallParams {
     // 1: the weights (W and its scales) were complete before the previous kernel on the
     // stream started, so the producer loads them before waiting for it
     int w_early;
+    // int8 operands: fp32 row scales of the activation and of the weight
+    const float* sx;
+    const float* sw;
+    // activation builds: y = bf16(act(v) + residual), over column pairs when gated
+    int act;
+    int gated;
+    int n_out;                 // columns of y and of the residual
+    const uint16_t* residual;  // bf16 [M, n_out] or null
     int* status;
     uint64_t budget_ns;
 };
@@ -134,7 +143,29 @@ __device__ __forceinline__ void small_step_w(uint32_t acc0, uint32_t acc1, uint6
     }
 }
 
-template <bool RSB, bool F32>
+// The int8 form of a K step (K = 32): no scales, both MMAs under one election.
+template <bool TWO>
+__device__ __forceinline__ void small_step_i8_w(uint32_t acc0, uint32_t acc1, uint64_t wd,
+                                                uint64_t xd, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (TWO) {
+        asm volatile(
+            "{\n\t"
+            ".reg .pred p, e;\n\t"
+            ".reg .b64 w1;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %5, 0;\n\t"
+            "add.u64 w1, %2, 1024;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::i8 [%0], %2, %3, %4, p;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::i8 [%1], w1, %3, %4, p;\n\t"
+            "}" ::"r"(acc0),
+            "r"(acc1), "l"(wd), "l"(xd), "r"(idesc), "r"(accumulate)
+            : "memory");
+    } else {
+        mma_i8_w(acc0, wd, xd, idesc, accumulate);
+    }
+}
+
+template <bool RSB, bool F32, bool I8 = false, bool ACT = false>
 __global__ void __launch_bounds__(XTHREADS, 1)
 gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                   const SmallParams p) {
@@ -179,6 +210,7 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         uint8_t* sW = smem + stage * XS_STAGE;
         uint8_t* sSFW = sW + XS_W + XS_X;
         tma_load_2d_w(sW, &tmW, &full[stage], kt * XBKB, tile * XW_ROWS);
+        if constexpr (I8) return;
         if constexpr (RSB) {
             bulk_load_w(sSFW, p.sfw + ((size_t)tile * p.k_tiles + kt) * 4096, 4096u, &full[stage]);
         } else {
@@ -189,6 +221,7 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         }
     };
     auto stage_bytes = [&](int steps) -> uint32_t {
+        if constexpr (I8) return XS_W + (uint32_t)p.mpad * XBKB;
         const uint32_t sfx_bytes = (uint32_t)steps * 512u;
         const uint32_t sfw_bytes = RSB ? 4096u : sfx_bytes * (two ? 2u : 1u);
         return XS_W + (uint32_t)p.mpad * XBKB + sfw_bytes + sfx_bytes;
@@ -234,7 +267,8 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 uint8_t* sSFX = sX + XS_X + XS_SFW;
                 const uint32_t sfx_bytes = (uint32_t)steps * 512u;
                 tma_load_2d_w(sX, &tmX, &full[stage], kt * XBKB, 0);
-                bulk_load_w(sSFX, p.sfx + (size_t)(4 * kt) * 512, sfx_bytes, &full[stage]);
+                if constexpr (!I8)
+                    bulk_load_w(sSFX, p.sfx + (size_t)(4 * kt) * 512, sfx_bytes, &full[stage]);
                 issued |= 1u << stage;
                 issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                 if (++stage == XSTAGES) {
@@ -276,7 +310,14 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                     if (kk < steps) {
                         const uint32_t sf_t = tmem + XTMEM_SF + 12u * (uint32_t)slot;
                         const uint32_t acc = (kt > kt_begin || kk > 0) ? 1u : 0u;
-                        if (two)
+                        if constexpr (I8) {
+                            if (two)
+                                small_step_i8_w<true>(tmem, tmem + XTMEM_ACC1, wd + 2 * kk,
+                                                      xd + 2 * kk, p.idesc, acc);
+                            else
+                                small_step_i8_w<false>(tmem, tmem + XTMEM_ACC1, wd + 2 * kk,
+                                                       xd + 2 * kk, p.idesc, acc);
+                        } else if (two)
                             small_step_w<true>(tmem, tmem + XTMEM_ACC1, wd + 2 * kk, xd + 2 * kk,
                                                p.idesc, sf_t, sfw_d + 32 * kk, sfx_d + 32 * kk, acc);
                         else
@@ -332,12 +373,32 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         const int G = p.M * (XW_ROWS / 4);
         const int lo = rank * G / splits, hi = (rank + 1) * G / splits;
         const uint32_t part = smem_u32(smem);
-        const float alpha = *p.alpha;
+        const float alpha = I8 ? 0.0f : *p.alpha;
         for (int idx = lo + (int)threadIdx.x - 64; idx < hi; idx += XTHREADS - 64) {
             const int m = idx >> 6, g = idx & 63;
             const int n = tile * XW_ROWS + 4 * g;
             if (n >= p.N) continue;
             const uint32_t off = part + (uint32_t)((m * XW_ROWS + 4 * g) * 4);
+            if constexpr (I8) {   // integer partial sums: exact in any order
+                int acc[4] = {0, 0, 0, 0};
+                for (int r = 0; r < splits; ++r) {
+                    const float4 t = ld_dsmem_f4(dsmem_addr(off, (uint32_t)r));
+                    acc[0] += __float_as_int(t.x);
+                    acc[1] += __float_as_int(t.y);
+                    acc[2] += __float_as_int(t.z);
+                    acc[3] += __float_as_int(t.w);
+                }
+                const float sx = p.sx[m];
+                float v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j] = __fmul_rn(__fmul_rn(__int2float_rn(acc[j]), sx), p.sw[min(n + j, p.N - 1)]);
+                    if (p.bias)
+                        v[j] = __fadd_rn(v[j], __uint_as_float((uint32_t)p.bias[min(n + j, p.N - 1)] << 16));
+                }
+                finish_granule(v, p.act, p.gated != 0, p.residual, p.y, m, n, p.n_out);
+                continue;
+            }
             float4 acc = ld_dsmem_f4(dsmem_addr(off, 0));
             for (int r = 1; r < splits; ++r) {
                 const float4 v = ld_dsmem_f4(dsmem_addr(off, (uint32_t)r));
@@ -353,7 +414,9 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 for (int j = 0; j < 4; ++j)
                     v[j] = __fadd_rn(v[j], __uint_as_float((uint32_t)p.bias[min(n + j, p.N - 1)] << 16));
             }
-            if constexpr (F32) {
+            if constexpr (ACT) {
+                finish_granule(v, p.act, p.gated != 0, p.residual, p.y, m, n, p.n_out);
+            } else if constexpr (F32) {
                 float* yp = p.y32 + (size_t)m * p.N + n;
                 for (int j = 0; j < 4 && n + j < p.N; ++j) yp[j] = v[j];
             } else {
@@ -394,11 +457,11 @@ cudaLaunchConfig_t small_config(int grid, int splits, cudaStream_t stream,
     return cfg;
 }
 
-template <bool RSB, bool F32>
+template <bool RSB, bool F32, bool I8, bool ACT>
 bool small_attr(int device) {
     static std::atomic<int> done[64];
     if (done[device & 63].load(std::memory_order_acquire)) return true;
-    if (cudaFuncSetAttribute(gemm_small_kernel<RSB, F32>,
+    if (cudaFuncSetAttribute(gemm_small_kernel<RSB, F32, I8, ACT>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, XSMEM) != cudaSuccess)
         return false;
     done[device & 63].store(1, std::memory_order_release);
@@ -407,7 +470,7 @@ bool small_attr(int device) {
 
 // K splits: the largest S <= 8 (a portable cluster) with S <= the K stages and
 // tiles * S <= SMs whose clusters are all resident at once (cached per device and S).
-template <bool RSB, bool F32>
+template <bool RSB, bool F32, bool I8, bool ACT>
 int small_splits(int tiles, int k_tiles, const DeviceInfo& dev) {
     static std::atomic<int> cap[64][9];   // max active clusters + 1 (0 = not queried yet)
     int smax = min(8, k_tiles);
@@ -418,7 +481,7 @@ int small_splits(int tiles, int k_tiles, const DeviceInfo& dev) {
             cudaLaunchAttribute attr[2];
             const cudaLaunchConfig_t cfg = small_config(sp * tiles, sp, nullptr, attr);
             int n = 0;
-            if (cudaOccupancyMaxActiveClusters(&n, gemm_small_kernel<RSB, F32>, &cfg) != cudaSuccess) {
+            if (cudaOccupancyMaxActiveClusters(&n, gemm_small_kernel<RSB, F32, I8, ACT>, &cfg) != cudaSuccess) {
                 (void)cudaGetLastError();
                 n = 0;
             }
@@ -430,22 +493,24 @@ int small_splits(int tiles, int k_tiles, const DeviceInfo& dev) {
     return 1;
 }
 
-template <bool RSB, bool F32>
+template <bool RSB, bool F32, bool I8 = false, bool ACT = false>
 nvfp4_status launch_small_impl(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
                                const uint8_t* sfb, const float* alpha, const void* bias, void* y,
                                int64_t M, int64_t N, int64_t K, cudaStream_t stream,
-                               bool weights_ready) {
+                               bool weights_ready, const float* sx = nullptr,
+                               const float* sw = nullptr, const EpilogueArgs* epi = nullptr) {
     DeviceInfo dev;
     nvfp4_status st = device_info(&dev);
     if (st != NVFP4_OK) return st;
     int* status = nullptr;
     if ((st = status_word(&status)) != NVFP4_OK) return st;
-    if (!small_attr<RSB, F32>(dev.device)) return NVFP4_ERR_CUDA;
+    if (!small_attr<RSB, F32, I8, ACT>(dev.device)) return NVFP4_ERR_CUDA;
 
     SmallParams p{};
     p.mpad = (int)((M + 15) / 16 * 16);
+    const int64_t kbytes = I8 ? K : K / 2;   // bytes of one operand row
     CUtensorMap mapW, mapX;
-    if (!make_operand_map(&mapW, b, N, K / 2, XW_ROWS) || !make_operand_map(&mapX, a, M, K / 2, p.mpad))
+    if (!make_operand_map(&mapW, b, N, kbytes, XW_ROWS) || !make_operand_map(&mapX, a, M, kbytes, p.mpad))
         return NVFP4_ERR_CUDA;
     p.sfw = sfb;
     p.sfx = sfa;
@@ -455,19 +520,28 @@ nvfp4_status launch_small_impl(const uint8_t* a, const uint8_t* sfa, const uint8
     p.y32 = F32 ? static_cast<float*>(y) : nullptr;
     p.M = (int)M;
     p.N = (int)N;
-    // E2M1 x E2M1, UE4M3 block scales, both K-major; N = padded M, M = 128
-    p.idesc = (1u << 7) | (1u << 10) | ((uint32_t)(p.mpad >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-    p.k_tiles = (int)((K / 2 + XBKB - 1) / XBKB);
-    p.kchunks = (int)(K / 64);
+    // E2M1 x E2M1, UE4M3 block scales, both K-major; N = padded M, M = 128.  int8: signed
+    // operands (format 1 both), int32 accumulator (D format 2).
+    p.idesc = (I8 ? 2u << 4 : 0u) | (1u << 7) | (1u << 10) | ((uint32_t)(p.mpad >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+    p.k_tiles = (int)((kbytes + XBKB - 1) / XBKB);
+    p.kchunks = (int)(kbytes / 32);          // 32-byte MMA K steps
     p.w_row_tiles = (int)((N + 127) / 128);
     p.w_early = weights_ready ? 1 : 0;
+    p.sx = sx;
+    p.sw = sw;
+    if (ACT) {
+        p.act = epi->activation;
+        p.gated = (epi->activation & NVFP4_ACT_GATED) ? 1 : 0;
+        p.n_out = (int)(p.gated ? N / 2 : N);
+        p.residual = static_cast<const uint16_t*>(epi->residual);
+    }
     p.status = status;
     p.budget_ns = 4000000000ull;   // 4 s
     const int tiles = (int)((N + XW_ROWS - 1) / XW_ROWS);
-    p.splits = small_splits<RSB, F32>(tiles, p.k_tiles, dev);
+    p.splits = small_splits<RSB, F32, I8, ACT>(tiles, p.k_tiles, dev);
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = small_config(tiles * p.splits, p.splits, stream, attr);
-    if (cudaLaunchKernelEx(&cfg, gemm_small_kernel<RSB, F32>, mapW, mapX, p) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, gemm_small_kernel<RSB, F32, I8, ACT>, mapW, mapX, p) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     return NVFP4_OK;
 }
@@ -485,6 +559,22 @@ nvfp4_status launch_gemm_small(const uint8_t* a, const uint8_t* sfa, const uint8
                        : launch_small_impl<true, false>(a, sfa, b, sfb, alpha, bias, y, M, N, K, stream, w);
     return f32_out ? launch_small_impl<false, true>(a, sfa, b, sfb, alpha, bias, y, M, N, K, stream, w)
                    : launch_small_impl<false, false>(a, sfa, b, sfb, alpha, bias, y, M, N, K, stream, w);
+}
+
+nvfp4_status launch_gemm_small_act(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
+                                   const uint8_t* sfb, bool int8, bool sfb_prepared,
+                                   const float* alpha, const float* sx, const float* sw,
+                                   const void* bias, const EpilogueArgs& epi, void* y, int64_t M,
+                                   int64_t N, int64_t K, cudaStream_t stream, bool weights_ready) {
+    if (M < 1 || M > kSmallMaxRows) return NVFP4_ERR_INVALID_ARG;
+    const bool w = weights_ready;
+    if (int8)
+        return launch_small_impl<false, false, true, true>(a, sfa, b, sfb, alpha, bias, y, M, N, K,
+                                                           stream, w, sx, sw, &epi);
+    return sfb_prepared ? launch_small_impl<true, false, false, true>(
+                              a, sfa, b, sfb, alpha, bias, y, M, N, K, stream, w, sx, sw, &epi)
+                        : launch_small_impl<false, false, false, true>(
+                              a, sfa, b, sfb, alpha, bias, y, M, N, K, stream, w, sx, sw, &epi);
 }
 
 }  // namespace nvfp4

@@ -109,6 +109,46 @@ nvfp4_status launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b,
                               const void* bias, void* y, int64_t M, int64_t N, int64_t K,
                               cudaStream_t stream);
 
+// Epilogue of the *_act products: an activation (plain, or gated over column pairs) and a
+// residual [M, N] (gated [M, N / 2]) added to it, or null.
+struct EpilogueArgs {
+    int activation;            // NVFP4_ACT_*, possibly with NVFP4_ACT_GATED
+    const void* residual;
+};
+
+nvfp4_status launch_gemm_act(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
+                             const uint8_t* sfb, bool sfb_prepared, const float* alpha,
+                             const void* bias, const EpilogueArgs& epi, void* y, int64_t M,
+                             int64_t N, int64_t K, cudaStream_t stream,
+                             bool weights_ready = false);
+nvfp4_status launch_int8_gemm_act(const int8_t* a, const float* sa, const int8_t* b,
+                                  const float* sb, const void* bias, const EpilogueArgs& epi,
+                                  void* y, int64_t M, int64_t N, int64_t K, cudaStream_t stream);
+
+// The swapped-operand kernel with the same epilogue, for NVFP4 (sfa, sfb, alpha) or int8
+// (sx, sw) operands; M <= kSmallMaxRows.
+nvfp4_status launch_gemm_small_act(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
+                                   const uint8_t* sfb, bool int8, bool sfb_prepared,
+                                   const float* alpha, const float* sx, const float* sw,
+                                   const void* bias, const EpilogueArgs& epi, void* y, int64_t M,
+                                   int64_t N, int64_t K, cudaStream_t stream, bool weights_ready);
+
+// Residual addition, root-mean-square norm and quantization of [rows, K] (norm.cu).
+constexpr int64_t kNormMaxK = 65536;   // 1024 threads x four 16-value units
+struct NormInputs {
+    const void* x;
+    const void* residual;      // or null
+    const void* weight;        // or null: ones
+    double eps;
+    int64_t rows, K;
+    void* residual_out;        // or null
+    void* norm_out;            // or null
+};
+nvfp4_status launch_int8_norm(const NormInputs& in, int8_t* q, float* scale, cudaStream_t stream);
+nvfp4_status launch_nvfp4_norm(const NormInputs& in, const float* gsf, uint8_t* packed,
+                               uint8_t* sf, const float* gsf_w, float* alpha_out,
+                               cudaStream_t stream);
+
 // NVFP4 -> bf16 expansion: y = bf16(fp32(E2M1 * E4M3) / gsf).
 nvfp4_status launch_dequantize(const uint8_t* packed, const uint8_t* sf, const float* gsf,
                                int64_t rows, int64_t K, void* y, cudaStream_t stream);

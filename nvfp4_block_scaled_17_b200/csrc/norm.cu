@@ -1,0 +1,319 @@
+// norm.cu -- residual addition, root-mean-square norm and quantization in one pass.
+//
+// What a transformer block does in front of a quantized linear:
+//     h = bf16(x + residual)                       (h = x without a residual)
+//     rstd = fp32(1 / sqrt(mean(h^2) + eps))       per row
+//     n = bf16(fp32(fp32(h * rstd) * w))
+// followed by the library's own encoding of n: per-row int8 codes (int8_quantize_rows) or
+// NVFP4 codes under a static global scale (nvfp4_quantize without rotation).  The codes
+// equal those of the separate passes on the bf16 n bit for bit.
+//
+// The sum of squares is kept in 64 bits: the square of a bf16 value is exact there and the
+// sum's relative error is below 2^-49 for any row, so rstd (one rounding to fp32) does not
+// depend on the order of the additions, and with it neither do the codes.
+//
+// Layout: a unit is 16 consecutive values of a row (one NVFP4 block; 32 bytes of bf16, 16
+// of int8 codes).  A thread owns C units of a row, lane-contiguous, so a row is read once
+// into registers and every store is 16 bytes wide (8 for FP4 codes).  Rows of up to 2048
+// values take one warp each (no block barrier); longer ones one block each.
+#include "common.cuh"
+#include "kernels.h"
+
+#include <atomic>
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kNormWarpThreads = 256;      // warp-per-row blocks: eight rows at a time
+
+struct NormParams {
+    const uint16_t* x;
+    const uint16_t* residual;   // or null
+    const uint16_t* weight;     // or null: ones
+    uint16_t* h_out;            // or null
+    uint16_t* n_out;            // or null
+    int64_t rows, rows_padded;  // rows_padded: rows of the scale layout (FP4), else rows
+    int64_t K;
+    int units;                  // K / 16
+    int units_padded;           // scale columns (FP4: to a multiple of four), else units
+    double inv_k, eps;
+    // int8
+    int8_t* q;
+    float* scale;
+    // NVFP4
+    const float* gsf;
+    const float* gsf_w;
+    float* alpha_out;
+    uint8_t* packed;
+    uint8_t* sf;
+    int64_t cgroups;            // four-block column groups of the scale layout
+};
+
+struct Unit {
+    uint32_t w[8];              // 16 bf16 values
+};
+
+__device__ __forceinline__ Unit load_unit(const uint16_t* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint4 b = *reinterpret_cast<const uint4*>(p + 8);
+    return Unit{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+
+__device__ __forceinline__ void store_unit(uint16_t* p, const Unit& u) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]);
+    *reinterpret_cast<uint4*>(p + 8) = make_uint4(u.w[4], u.w[5], u.w[6], u.w[7]);
+}
+
+__device__ __forceinline__ uint32_t unit_absmax(const Unit& u) {
+    return absmax2_bf16(absmax2_bf16(absmax2_bf16(u.w[0], u.w[1]), absmax2_bf16(u.w[2], u.w[3])),
+                        absmax2_bf16(absmax2_bf16(u.w[4], u.w[5]), absmax2_bf16(u.w[6], u.w[7])));
+}
+
+// 16 int8 codes of a unit under the row scale s; r = rn(1 / s).  rn(n / s) by one
+// remainder step (Markstein), as int8_quantize_rows computes it; a subnormal s, whose
+// reciprocal would overflow, takes the division, and s = 0 gives zeros.
+__device__ __forceinline__ uint4 int8_codes(const Unit& u, float s, float r, bool fast) {
+    uint32_t out[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        int c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t word = u.w[2 * g + (j >> 1)];
+            const float v = (j & 1) ? bf16hi(word) : bf16lo(word);
+            float t;
+            if (fast) {
+                const float q0 = __fmul_rn(v, r);
+                t = __fmaf_rn(__fmaf_rn(-q0, s, v), r, q0);
+            } else {
+                t = s != 0.0f ? __fdiv_rn(v, s) : 0.0f;
+            }
+            c[j] = __float2int_rn(t);
+        }
+        out[g] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// One block of 16 values as nvfp4_quantize encodes it under a static global scale.
+__device__ __forceinline__ uint32_t fp4_codes(const Unit& u, float gsf, uint2& codes) {
+    const uint32_t s8 = e4m3_scale_of_scaled_max(__fmul_rn(gsf, absmax_of_pair(unit_absmax(u))));
+    const float inv = (s8 == 0u || s8 == 127u) ? 0.0f : __fdiv_rn(gsf, f32_from_e4m3(s8));
+    float v[2][8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        v[j >> 2][2 * (j & 3)] = __fmul_rn(bf16lo(u.w[j]), inv);
+        v[j >> 2][2 * (j & 3) + 1] = __fmul_rn(bf16hi(u.w[j]), inv);
+    }
+    codes.x = s8 ? e2m1x8_from_f32(v[0]) : 0u;
+    codes.y = s8 ? e2m1x8_from_f32(v[1]) : 0u;
+    return s8;
+}
+
+// C units per thread; BLOCK: a row per block (blockDim.x threads), else a row per warp.
+template <bool FP4, int C, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? 1024 : kNormWarpThreads) norm_kernel(const NormParams p) {
+    __shared__ double red_ss[32];
+    __shared__ uint32_t red_mx[32];
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int span = BLOCK ? (int)blockDim.x : 32;         // threads of a row
+    const int tid = BLOCK ? (int)threadIdx.x : lane;
+    const int warps = (int)blockDim.x >> 5;
+    const int64_t first = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * warps + warp;
+    const int64_t step = BLOCK ? (int64_t)gridDim.x : (int64_t)gridDim.x * warps;
+    const float gsf = FP4 ? *p.gsf : 0.0f;
+    if (FP4 && p.alpha_out && blockIdx.x == 0 && threadIdx.x == 0)
+        *p.alpha_out = __frcp_rn(__fmul_rn(gsf, *p.gsf_w));
+
+    for (int64_t row = first; row < p.rows_padded; row += step) {
+        if (FP4 && row >= p.rows) {                        // padding rows of the scale layout
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int u = i * span + tid;
+                if (u < p.units_padded)
+                    p.sf[((row >> 7) * p.cgroups + (u >> 2)) * 512 + ((row & 31) << 4) +
+                         (((row >> 5) & 3) << 2) + (u & 3)] = 0;
+            }
+            continue;
+        }
+        Unit h[C];
+        double ss0 = 0.0, ss1 = 0.0;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int u = i * span + tid;
+            if (u < p.units) h[i] = load_unit(p.x + row * p.K + 16 * (int64_t)u);
+            else h[i] = Unit{};
+        }
+        if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int u = i * span + tid;
+                if (u >= p.units) continue;
+                const int64_t at = row * p.K + 16 * (int64_t)u;
+                const Unit r = load_unit(p.residual + at);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    h[i].w[j] = bf16x2_rn(__fadd_rn(bf16lo(h[i].w[j]), bf16lo(r.w[j])),
+                                          __fadd_rn(bf16hi(h[i].w[j]), bf16hi(r.w[j])));
+                if (p.h_out) store_unit(p.h_out + at, h[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const double a = (double)bf16lo(h[i].w[j]), b = (double)bf16hi(h[i].w[j]);
+                ss0 = fma(a, a, ss0);
+                ss1 = fma(b, b, ss1);
+            }
+        double ss = ss0 + ss1;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if constexpr (BLOCK) {
+            if (lane == 0) red_ss[warp] = ss;
+            __syncthreads();
+            ss = lane < warps ? red_ss[lane] : 0.0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        }
+        const float rstd = (float)rsqrt(ss * p.inv_k + p.eps);
+
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int u = i * span + tid;
+            Unit w{{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u,
+                    0x3f803f80u, 0x3f803f80u}};
+            if (p.weight && u < p.units) w = load_unit(p.weight + 16 * (int64_t)u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                h[i].w[j] = bf16x2_rn(__fmul_rn(__fmul_rn(bf16lo(h[i].w[j]), rstd), bf16lo(w.w[j])),
+                                      __fmul_rn(__fmul_rn(bf16hi(h[i].w[j]), rstd), bf16hi(w.w[j])));
+            if (p.n_out && u < p.units) store_unit(p.n_out + row * p.K + 16 * (int64_t)u, h[i]);
+            if constexpr (!FP4) m = absmax2_bf16(m, unit_absmax(h[i]));
+        }
+        if constexpr (FP4) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int u = i * span + tid;
+                uint2 codes = make_uint2(0u, 0u);
+                uint32_t s8 = 0u;
+                if (u < p.units) {
+                    s8 = fp4_codes(h[i], gsf, codes);
+                    *reinterpret_cast<uint2*>(p.packed + row * (p.K / 2) + 8 * (int64_t)u) = codes;
+                }
+                if (u < p.units_padded)
+                    p.sf[((row >> 7) * p.cgroups + (u >> 2)) * 512 + ((row & 31) << 4) +
+                         (((row >> 5) & 3) << 2) + (u & 3)] = (uint8_t)s8;
+            }
+        } else {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = absmax2_bf16(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if constexpr (BLOCK) {
+                if (lane == 0) red_mx[warp] = m;
+                __syncthreads();
+                m = lane < warps ? red_mx[lane] : 0u;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    m = absmax2_bf16(m, __shfl_xor_sync(0xffffffffu, m, o));
+            }
+            const float s = __fdiv_rn(absmax_of_pair(m), 127.0f);
+            if (tid == 0) p.scale[row] = s;
+            const bool fast = s >= 1.17549435e-38f;
+            const float r = fast ? __frcp_rn(s) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int u = i * span + tid;
+                if (u < p.units)
+                    *reinterpret_cast<uint4*>(p.q + row * p.K + 16 * (int64_t)u) =
+                        int8_codes(h[i], s, r, fast);
+            }
+        }
+        if constexpr (FP4 && BLOCK) __syncthreads();   // red_ss is free for the next row
+    }
+}
+
+template <bool FP4, int C, bool BLOCK>
+nvfp4_status launch_norm(const NormParams& p, int threads, const DeviceInfo& dev,
+                         cudaStream_t stream) {
+    static std::atomic<int> per_sm[64][33];    // resident blocks, by warps of a block
+    std::atomic<int>& cell = per_sm[dev.device & 63][threads / 32];
+    int resident = cell.load(std::memory_order_relaxed);
+    if (!resident) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, norm_kernel<FP4, C, BLOCK>,
+                                                          threads, 0) != cudaSuccess ||
+            resident <= 0)
+            return NVFP4_ERR_CUDA;
+        cell.store(resident, std::memory_order_relaxed);
+    }
+    const int per_block = BLOCK ? 1 : threads / 32;
+    const int64_t need = (p.rows_padded + per_block - 1) / per_block;
+    const int64_t cap = (int64_t)dev.sms * resident;
+    const unsigned grid = (unsigned)(need < cap ? need : cap);
+    return launch_pdl(norm_kernel<FP4, C, BLOCK>, grid, (unsigned)threads, 0, stream, p) ==
+                   cudaSuccess
+               ? NVFP4_OK
+               : NVFP4_ERR_CUDA;
+}
+
+template <bool FP4>
+nvfp4_status dispatch_norm(const NormParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+    const int U = p.units_padded;
+    if (U <= 32) return launch_norm<FP4, 1, false>(p, kNormWarpThreads, dev, stream);
+    if (U <= 64) return launch_norm<FP4, 2, false>(p, kNormWarpThreads, dev, stream);
+    if (U <= 128) return launch_norm<FP4, 4, false>(p, kNormWarpThreads, dev, stream);
+    if (U <= 1024) return launch_norm<FP4, 1, true>(p, (U + 31) / 32 * 32, dev, stream);
+    if (U <= 2048) return launch_norm<FP4, 2, true>(p, ((U + 1) / 2 + 31) / 32 * 32, dev, stream);
+    return launch_norm<FP4, 4, true>(p, ((U + 3) / 4 + 31) / 32 * 32, dev, stream);
+}
+
+NormParams norm_params(const NormInputs& in) {
+    NormParams p{};
+    p.x = static_cast<const uint16_t*>(in.x);
+    p.residual = static_cast<const uint16_t*>(in.residual);
+    p.weight = static_cast<const uint16_t*>(in.weight);
+    p.h_out = static_cast<uint16_t*>(in.residual_out);
+    p.n_out = static_cast<uint16_t*>(in.norm_out);
+    p.rows = p.rows_padded = in.rows;
+    p.K = in.K;
+    p.units = p.units_padded = (int)(in.K / 16);
+    p.inv_k = 1.0 / (double)in.K;
+    p.eps = in.eps;
+    return p;
+}
+
+}  // namespace
+
+nvfp4_status launch_int8_norm(const NormInputs& in, int8_t* q, float* scale, cudaStream_t stream) {
+    DeviceInfo dev;
+    nvfp4_status st = device_info(&dev);
+    if (st != NVFP4_OK) return st;
+    NormParams p = norm_params(in);
+    p.q = q;
+    p.scale = scale;
+    return dispatch_norm<false>(p, dev, stream);
+}
+
+nvfp4_status launch_nvfp4_norm(const NormInputs& in, const float* gsf, uint8_t* packed,
+                               uint8_t* sf, const float* gsf_w, float* alpha_out,
+                               cudaStream_t stream) {
+    DeviceInfo dev;
+    nvfp4_status st = device_info(&dev);
+    if (st != NVFP4_OK) return st;
+    NormParams p = norm_params(in);
+    p.gsf = gsf;
+    p.gsf_w = gsf_w;
+    p.alpha_out = alpha_out;
+    p.packed = packed;
+    p.sf = sf;
+    p.rows_padded = (in.rows + 127) / 128 * 128;
+    p.units_padded = (p.units + 3) / 4 * 4;
+    p.cgroups = p.units_padded / 4;
+    return dispatch_norm<true>(p, dev, stream);
+}
+
+}  // namespace nvfp4
