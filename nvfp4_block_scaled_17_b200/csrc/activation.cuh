@@ -83,8 +83,49 @@ __device__ __forceinline__ void apply_activation(float (&v)[N], int act, bool ga
     }
 }
 
-// Four consecutive columns (n % 4 == 0) of an output row, from the reduction phases of the
-// split-K builds: activation, residual, one rounding, store.  n_out: columns of y.
+// Four consecutive columns (n % 4 == 0) of an output row, summed over the partial tiles of a
+// cluster (at shared offset `off` of each of its CTAs, in rank order; int8 sums are exact in
+// any order), scaled and biased.
+template <bool I8>
+__device__ __forceinline__ void reduce_granule(float (&v)[4], uint32_t off, int splits, float alpha,
+                                               float sx, const float* sw, const uint16_t* bias, int n,
+                                               int N) {
+    float4 t = ld_dsmem_f4(dsmem_addr(off, 0));
+    if constexpr (I8) {
+        int acc[4] = {__float_as_int(t.x), __float_as_int(t.y), __float_as_int(t.z), __float_as_int(t.w)};
+        for (int r = 1; r < splits; ++r) {
+            t = ld_dsmem_f4(dsmem_addr(off, (uint32_t)r));
+            acc[0] += __float_as_int(t.x);
+            acc[1] += __float_as_int(t.y);
+            acc[2] += __float_as_int(t.z);
+            acc[3] += __float_as_int(t.w);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = __fmul_rn(__fmul_rn(__int2float_rn(acc[j]), sx), sw[min(n + j, N - 1)]);
+    } else {
+        v[0] = t.x;
+        v[1] = t.y;
+        v[2] = t.z;
+        v[3] = t.w;
+        for (int r = 1; r < splits; ++r) {
+            t = ld_dsmem_f4(dsmem_addr(off, (uint32_t)r));
+            v[0] = __fadd_rn(v[0], t.x);
+            v[1] = __fadd_rn(v[1], t.y);
+            v[2] = __fadd_rn(v[2], t.z);
+            v[3] = __fadd_rn(v[3], t.w);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __fmul_rn(alpha, v[j]);
+    }
+    if (bias) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = __fadd_rn(v[j], __uint_as_float((uint32_t)bias[min(n + j, N - 1)] << 16));
+    }
+}
+
+// The rest of such a granule: activation, residual, one rounding, store.  n_out: columns of y.
 __device__ __forceinline__ void finish_granule(float (&v)[4], int act, bool gated,
                                                const uint16_t* residual, uint16_t* y, int64_t row,
                                                int n, int n_out) {

@@ -452,8 +452,9 @@ nvfp4_status nvfp4_gemm_act(const uint8_t* a, const uint8_t* sfa, const uint8_t*
     nvfp4_status st = device_info(&dev);
     if (st != NVFP4_OK) return st;
     if (M == 0 || N == 0) return NVFP4_OK;
-    return launch_gemm_act(a, sfa, b, sfb, sfb_prepared != 0, alpha, bias, {activation, residual},
-                           y, M, N, K, static_cast<cudaStream_t>(stream));
+    return launch_gemm_act({false, a, b, sfa, sfb, sfb_prepared != 0, alpha, nullptr, nullptr, bias,
+                            {activation, residual}, y, M, N, K, false},
+                           static_cast<cudaStream_t>(stream));
 }
 
 nvfp4_status nvfp4_linear_act(const void* x, int64_t M, int64_t K, const uint8_t* w_packed,
@@ -489,8 +490,9 @@ nvfp4_status nvfp4_linear_act(const void* x, int64_t M, int64_t K, const uint8_t
     st = launch_quantize(x, M, K, group, gsf_x, &scalars[0], xp, xsf, partials, gsf_w, &scalars[1],
                          s);
     if (st != NVFP4_OK) return st;
-    return launch_gemm_act(xp, xsf, w_packed, w_sf, w_sf_prepared != 0, &scalars[1], bias,
-                           {activation, residual}, y, M, N, K, s, true);
+    return launch_gemm_act({false, xp, w_packed, xsf, w_sf, w_sf_prepared != 0, &scalars[1], nullptr,
+                            nullptr, bias, {activation, residual}, y, M, N, K, true},
+                           s);
 }
 
 nvfp4_status int8_gemm_act(const int8_t* a, const float* sa, const int8_t* b, const float* sb,
@@ -507,8 +509,10 @@ nvfp4_status int8_gemm_act(const int8_t* a, const float* sa, const int8_t* b, co
     nvfp4_status st = device_info(&dev);
     if (st != NVFP4_OK) return st;
     if (M == 0 || N == 0) return NVFP4_OK;
-    return launch_int8_gemm_act(a, sa, b, sb, bias, {activation, residual}, y, M, N, K,
-                                static_cast<cudaStream_t>(stream));
+    return launch_gemm_act({true, reinterpret_cast<const uint8_t*>(a),
+                            reinterpret_cast<const uint8_t*>(b), nullptr, nullptr, false, nullptr, sa,
+                            sb, bias, {activation, residual}, y, M, N, K, false},
+                           static_cast<cudaStream_t>(stream));
 }
 
 nvfp4_status int8_linear_act(const void* x, int64_t M, int64_t K, const int8_t* wq,
@@ -535,7 +539,10 @@ nvfp4_status int8_linear_act(const void* x, int64_t M, int64_t K, const int8_t* 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     st = launch_int8_quantize_rows(x, M, K, xq, sx, s);
     if (st != NVFP4_OK) return st;
-    return launch_int8_gemm_act(xq, sx, wq, sw, bias, {activation, residual}, y, M, N, K, s);
+    return launch_gemm_act({true, reinterpret_cast<const uint8_t*>(xq),
+                            reinterpret_cast<const uint8_t*>(wq), nullptr, nullptr, false, nullptr, sx,
+                            sw, bias, {activation, residual}, y, M, N, K, false},
+                           s);
 }
 
 // The arguments that both norm entry points share.

@@ -79,18 +79,15 @@ constexpr int SMEM_BIAS = EPI_WARPS * 256;   // each epilogue warp's 128 bias va
 // Shared memory of one build.  B scales per stage: four 512-byte chunks per 128-row half,
 // copied from the 128x4 layout (two bulk copies) or, with RSB (prepared weight scales),
 // as the stage's one 4 KiB block, already in this order.
-// The activation builds (ACT) rotate three staging tiles per epilogue warp, which also
-// receive the residual, each on a barrier of its own.
-template <bool RSB, bool ACT = false>
+template <bool RSB>
 struct GemmSmem {
     static constexpr int SFB = 4 * 1024;
-    static constexpr int STG_BUFS = ACT ? 3 : 2;
+    static constexpr int STG_BUFS = 2;
     static constexpr int STG = EPI_WARPS * STG_BUFS * STG_BYTES;
     static constexpr int BYTES =
-        1024 + STAGES * (SMEM_A + SMEM_B + SMEM_SFA + SFB) + STG + SMEM_BIAS + (ACT ? 512 : 256);
+        1024 + STAGES * (SMEM_A + SMEM_B + SMEM_SFA + SFB) + STG + SMEM_BIAS + 256;
 };
-static_assert(GemmSmem<false>::BYTES <= 232448 && GemmSmem<true>::BYTES <= 232448 &&
-                  GemmSmem<false, true>::BYTES <= 232448,
+static_assert(GemmSmem<false>::BYTES <= 232448 && GemmSmem<true>::BYTES <= 232448,
               "dynamic shared memory above the 227 KiB a CTA can have");
 constexpr int TMEM_COLS = 512;
 constexpr uint32_t TMEM_BUF1 = 192;     // second accumulator buffer (overlaps [192, 256))
@@ -132,7 +129,7 @@ struct GemmParams {
     // 1: the weight operand (B and its scales) was complete before the previous kernel on
     // the stream started, so the producer loads the first stages' B before waiting for it
     int w_early;
-    // activation builds: y = bf16(act(v) + residual), or over column pairs when gated
+    // activation build (split-K only): y = bf16(act(v) + residual), over column pairs when gated
     int act;                   // NVFP4_ACT_*
     int gated;
     int n_out;                 // columns of y and of the residual: N, gated N / 2
@@ -185,9 +182,9 @@ __device__ __forceinline__ void tile_coords(const GemmParams& p, int tile, int& 
 template <bool QOUT, bool I8, bool SPLITK, bool RSB, bool F32 = false, bool ACT = false>
 __global__ void __launch_bounds__(THREADS, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-            const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmR,
-            const GemmParams p) {
-    using SM = GemmSmem<RSB, ACT>;
+            const __grid_constant__ CUtensorMap tmY, const GemmParams p) {
+    static_assert(!ACT || SPLITK, "whole tiles with an activation run in gemm_pair.cu");
+    using SM = GemmSmem<RSB>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -205,14 +202,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     uint64_t* drain = ovl_free + 1;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-    uint64_t* res_full = drain + 2;          // ACT: [EPI_WARPS][STG_BUFS], residual tiles
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        if constexpr (ACT)
-            for (int s = 0; s < EPI_WARPS * SM::STG_BUFS; ++s) mbar_init(&res_full[s], 1);
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -405,45 +399,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         int stg_sel = 0;
         int it = 0;
         bool ok = true;
-        // ACT: the warp's output chunks (32 columns of y) in the order it writes them, four
-        // per tile, or two when gated.  With a residual, chunk k's residual is brought into
-        // staging tile k % 3 by TMA two chunks ahead, and the output replaces it there.
-        uint64_t* rfull = res_full + (warp - 2) * SM::STG_BUFS;
-        const bool res_tma = ACT && !SPLITK && p.residual && p.tma_store;
-        const int per_tile = p.gated ? 2 : 4;
-        int pf_tile = tile_first, pf_it = 0, pf_i = 0, pf_buf = 0;   // next residual to load
-        int pf_ahead = 0;                                            // loaded, not yet used
-        uint32_t res_phase = 0;
-        auto out_col = [&](int n_blk, int parity, int i) {
-            const int g = p.gated ? 2 * i : i & ~1, sub = p.gated ? 0 : i & 1;
-            const int c = (parity == 0 && half == 1) ? ((g + 2) & 3) + 4 + sub : half * 4 + g + sub;
-            return p.gated ? (n_blk * BN + c * 32) >> 1 : n_blk * BN + c * 32;
-        };
-        auto prefetch_residual = [&]() {
-            while (pf_tile < num_tiles) {
-                int m_blk, n_blk;
-                tile_coords(p, p.tile_base + pf_tile, m_blk, n_blk);
-                const int col = out_col(n_blk, pf_it & 1, pf_i);
-                if (++pf_i == per_tile) {
-                    pf_i = 0;
-                    ++pf_it;
-                    pf_tile += tile_step;
-                }
-                if (col >= p.n_out) continue;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&rfull[pf_buf], STG_BYTES);
-                    tma_load_2d(stg + pf_buf * STG_BYTES, &tmR, &rfull[pf_buf], col,
-                                m_blk * BM + quad * 32);
-                }
-                pf_buf = pf_buf == SM::STG_BUFS - 1 ? 0 : pf_buf + 1;
-                ++pf_ahead;
-                return;
-            }
-        };
-        if (res_tma) {
-            prefetch_residual();
-            prefetch_residual();
-        }
         for (int tile = tile_first; ok && tile < num_tiles; tile += tile_step, ++it) {
             int m_blk, n_blk;
             tile_coords(p, p.tile_base + tile, m_blk, n_blk);
@@ -557,100 +512,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if (n0 + j < p.N) yrow[n0 + j] = v;
                 }
             };
-            // ACT: scale, bias and activation of one chunk, in place (gated: at even places)
-            auto act_values = [&](uint32_t (&r)[32], int n0) {
-                float v[32];
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    if constexpr (I8) {
-                        const float2 sw2 = (n0 + j + 1 < p.N)
-                                               ? *reinterpret_cast<const float2*>(p.sw + n0 + j)
-                                               : make_float2(p.sw[min(n0 + j, p.N - 1)],
-                                                             p.sw[min(n0 + j + 1, p.N - 1)]);
-                        v[j] = __fmul_rn(__fmul_rn(__int2float_rn((int)r[j]), sx_row), sw2.x);
-                        v[j + 1] = __fmul_rn(__fmul_rn(__int2float_rn((int)r[j + 1]), sx_row), sw2.y);
-                    } else {
-                        v[j] = __fmul_rn(alpha, __uint_as_float(r[j]));
-                        v[j + 1] = __fmul_rn(alpha, __uint_as_float(r[j + 1]));
-                    }
-                }
-                if (p.bias) {
-                    const uint4* bp = reinterpret_cast<const uint4*>(sbias + (n0 - n_half) / 2);
-#pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        const uint4 w = bp[q4];
-                        const uint32_t bw[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            v[8 * q4 + 2 * j] = __fadd_rn(v[8 * q4 + 2 * j], bf16lo(bw[j]));
-                            v[8 * q4 + 2 * j + 1] = __fadd_rn(v[8 * q4 + 2 * j + 1], bf16hi(bw[j]));
-                        }
-                    }
-                }
-                apply_activation(v, p.act, p.gated != 0);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(v[j]);
-            };
-            // ACT: the residual's addition, the rounding and the store of one output chunk,
-            // whose values are u(0) .. u(31), at column col.
-            auto act_store = [&](auto u, int col) -> bool {
-                if (!p.tma_store) {
-                    const int row = row0 + lane;
-                    if (row < p.M) {
-                        const size_t at = (size_t)row * p.n_out + col;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (col + j < p.n_out) {
-                                float t = u(j);
-                                if (p.residual)
-                                    t = __fadd_rn(t, __uint_as_float((uint32_t)p.residual[at + j] << 16));
-                                p.y[at + j] = (uint16_t)bf16x2_rn(t, 0.0f);
-                            }
-                    }
-                    return true;
-                }
-                uint8_t* sb = stg + stg_sel * STG_BYTES;
-                if (res_tma) {
-                    if (!mbar_wait_bounded(&rfull[stg_sel], (res_phase >> stg_sel) & 1, abort_flag,
-                                           p.status, p.budget_ns))
-                        return false;
-                    res_phase ^= 1u << stg_sel;
-                    --pf_ahead;
-                } else {
-                    if (lane == 0) bulk_wait_read<2>();   // this tile's last store has read it
-                    __syncwarp();
-                }
-                // 64-byte swizzle: 16-byte chunk c of row r sits at c ^ ((r >> 1) & 3)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint4* at = reinterpret_cast<uint4*>(sb + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
-                    uint32_t w[4];
-                    if (res_tma) {
-                        const uint4 t = *at;
-                        const uint32_t rw[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            w[j] = bf16x2_rn(__fadd_rn(u(8 * c + 2 * j), bf16lo(rw[j])),
-                                             __fadd_rn(u(8 * c + 2 * j + 1), bf16hi(rw[j])));
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) w[j] = bf16x2_rn(u(8 * c + 2 * j), u(8 * c + 2 * j + 1));
-                    }
-                    *at = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    tma_store_2d(&tmY, sb, col, row0);
-                    bulk_commit();
-                }
-                stg_sel = stg_sel == SM::STG_BUFS - 1 ? 0 : stg_sel + 1;
-                if (res_tma) {
-                    if (lane == 0) bulk_wait_read<1>();   // the store before this one has read its tile
-                    prefetch_residual();
-                }
-                return true;
-            };
             // Two chunks at a time: both tensor-memory loads are in flight together, and
             // the columns are released as soon as they are in registers -- the shared
             // columns first, so the next tile's MMAs start before this tile is stored.
@@ -693,20 +554,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     store_f32(r1, n01);
                     continue;
                 }
-                if constexpr (ACT) {
-                    if (n00 < p.N) act_values(r0, n00);   // warp-uniform
-                    if (n01 < p.N) act_values(r1, n01);
-                    if (p.gated) {
-                        if (ok && n00 < p.N)
-                            ok = act_store([&](int j) {
-                                return __uint_as_float(j < 16 ? r0[2 * (j & 15)] : r1[2 * (j & 15)]);
-                            }, n00 >> 1);
-                    } else {
-                        if (ok && n00 < p.N) ok = act_store([&](int j) { return __uint_as_float(r0[j]); }, n00);
-                        if (ok && n01 < p.N) ok = act_store([&](int j) { return __uint_as_float(r1[j]); }, n01);
-                    }
-                    continue;
-                }
                 uint32_t w0[16], w1[16];
                 if (n00 < p.N) make_words(r0, n00, w0);   // warp-uniform
                 if (n01 < p.N) make_words(r1, n01, w1);
@@ -737,12 +584,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 }
             }
         }
-        // residual tiles still on their way must land before the block can exit
-        for (int s = pf_buf; ACT && pf_ahead > 0; --pf_ahead) {
-            s = s == 0 ? SM::STG_BUFS - 1 : s - 1;
-            volatile int no_abort = 0;
-            mbar_wait_bounded(&rfull[s], (res_phase >> s) & 1, &no_abort, p.status, p.budget_ns);
-        }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
     }
@@ -771,39 +612,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 if constexpr (ACT) {
                     const int64_t grow = (int64_t)m_blk * BM + row;
                     float v[4];
-                    if constexpr (I8) {   // integer partial sums: exact in any order
-                        int acc[4] = {0, 0, 0, 0};
-                        for (int r = 0; r < splits; ++r) {
-                            const float4 t = ld_dsmem_f4(dsmem_addr(off, (uint32_t)r));
-                            acc[0] += __float_as_int(t.x);
-                            acc[1] += __float_as_int(t.y);
-                            acc[2] += __float_as_int(t.z);
-                            acc[3] += __float_as_int(t.w);
-                        }
-                        const float sx = p.sx[grow];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            v[j] = __fmul_rn(__fmul_rn(__int2float_rn(acc[j]), sx),
-                                             p.sw[min(col + j, p.N - 1)]);
-                    } else {
-                        float4 acc = ld_dsmem_f4(dsmem_addr(off, 0));
-                        for (int r = 1; r < splits; ++r) {
-                            const float4 t = ld_dsmem_f4(dsmem_addr(off, (uint32_t)r));
-                            acc.x = __fadd_rn(acc.x, t.x);
-                            acc.y = __fadd_rn(acc.y, t.y);
-                            acc.z = __fadd_rn(acc.z, t.z);
-                            acc.w = __fadd_rn(acc.w, t.w);
-                        }
-                        v[0] = __fmul_rn(alpha, acc.x);
-                        v[1] = __fmul_rn(alpha, acc.y);
-                        v[2] = __fmul_rn(alpha, acc.z);
-                        v[3] = __fmul_rn(alpha, acc.w);
-                    }
-                    if (p.bias) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            v[j] = __fadd_rn(v[j], __uint_as_float((uint32_t)p.bias[min(col + j, p.N - 1)] << 16));
-                    }
+                    reduce_granule<I8>(v, off, splits, alpha, I8 ? p.sx[grow] : 0.0f, p.sw, p.bias, col,
+                                       p.N);
                     finish_granule(v, p.act, p.gated != 0, p.residual, p.y, grow, col, p.n_out);
                     continue;
                 }
@@ -846,6 +656,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     }
 }
 
+}  // namespace
+
 // bf16 [M, N] output with a 32 x 32 box and 64-byte swizzle (N % 8 == 0).
 bool make_output_map(CUtensorMap* map, void* base, int64_t M, int64_t N) {
     auto enc = tensor_map_encoder();
@@ -859,8 +671,6 @@ bool make_output_map(CUtensorMap* map, void* base, int64_t M, int64_t N) {
                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
-
-}  // namespace
 
 // 2-D uint8 view [rows, row_bytes] with a [box_rows, 128-byte] box, 128-byte swizzle.
 bool make_operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t row_bytes,
@@ -888,13 +698,13 @@ struct QuantOut {
 };
 
 // Split-K build: clusters of `splits` CTAs, one tile per cluster.
-template <bool RSB, bool ACT>
+template <bool RSB>
 cudaLaunchConfig_t split_k_config(int grid, int splits, cudaStream_t stream,
                                   cudaLaunchAttribute* attr, bool pdl = false) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = GemmSmem<RSB, ACT>::BYTES;
+    cfg.dynamicSmemBytes = GemmSmem<RSB>::BYTES;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)splits;
@@ -913,7 +723,7 @@ bool split_k_attr(int device) {
     if (done[device & 63].load(std::memory_order_acquire)) return true;
     if (cudaFuncSetAttribute(gemm_kernel<false, I8, true, RSB, F32, ACT>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             GemmSmem<RSB, ACT>::BYTES) != cudaSuccess)
+                             GemmSmem<RSB>::BYTES) != cudaSuccess)
         return false;
     done[device & 63].store(1, std::memory_order_release);
     return true;
@@ -932,7 +742,7 @@ int choose_splits(int tiles, int k_tiles, const DeviceInfo& dev) {
         int c = cap[dev.device & 63][sp].load(std::memory_order_relaxed) - 1;
         if (c < 0) {
             cudaLaunchAttribute attr[2];
-            const cudaLaunchConfig_t cfg = split_k_config<RSB, ACT>(sp * tiles, sp, nullptr, attr);
+            const cudaLaunchConfig_t cfg = split_k_config<RSB>(sp * tiles, sp, nullptr, attr);
             int n = 0;
             if (cudaOccupancyMaxActiveClusters(&n, gemm_kernel<false, I8, true, RSB, F32, ACT>, &cfg) !=
                 cudaSuccess) {
@@ -949,11 +759,11 @@ int choose_splits(int tiles, int k_tiles, const DeviceInfo& dev) {
 
 template <bool I8, bool RSB, bool F32, bool ACT>
 nvfp4_status launch_split_k(const CUtensorMap& mapA, const CUtensorMap& mapB,
-                            const CUtensorMap& mapY, const CUtensorMap& mapR, const GemmParams& p,
-                            int grid, int splits, cudaStream_t stream) {
+                            const CUtensorMap& mapY, const GemmParams& p, int grid, int splits,
+                            cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = split_k_config<RSB, ACT>(grid, splits, stream, attr, true);
-    if (cudaLaunchKernelEx(&cfg, gemm_kernel<false, I8, true, RSB, F32, ACT>, mapA, mapB, mapY, mapR, p) !=
+    const cudaLaunchConfig_t cfg = split_k_config<RSB>(grid, splits, stream, attr, true);
+    if (cudaLaunchKernelEx(&cfg, gemm_kernel<false, I8, true, RSB, F32, ACT>, mapA, mapB, mapY, p) !=
         cudaSuccess)
         return NVFP4_ERR_CUDA;
     return NVFP4_OK;
@@ -962,14 +772,13 @@ nvfp4_status launch_split_k(const CUtensorMap& mapA, const CUtensorMap& mapB,
 // One launcher for the builds of the kernel: NVFP4 (sfa = 128x4 scales; sfb = 128x4
 // scales, or with RSB the prepared weight scales; alpha), NVFP4 with the quantized
 // output, int8 (sfa/sfb unused; sx/sw = fp32 row scales of A and B), and (F32) the
-// NVFP4 GEMM with an unrounded fp32 output y.  ACT: the builds with an activation and a
-// residual in the epilogue (epi).
-template <bool QOUT, bool I8, bool RSB = false, bool F32 = false, bool ACT = false>
+// NVFP4 GEMM with an unrounded fp32 output y.
+template <bool QOUT, bool I8, bool RSB = false, bool F32 = false>
 nvfp4_status launch_gemm_impl(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
                               const uint8_t* sfb, const float* alpha, const void* bias, void* y,
                               int64_t M, int64_t N, int64_t K, const QuantOut* q,
                               const float* sx, const float* sw, cudaStream_t stream,
-                              bool weights_ready = false, const EpilogueArgs* epi = nullptr) {
+                              bool weights_ready = false) {
     DeviceInfo dev;
     nvfp4_status st = device_info(&dev);
     if (st != NVFP4_OK) return st;
@@ -977,37 +786,27 @@ nvfp4_status launch_gemm_impl(const uint8_t* a, const uint8_t* sfa, const uint8_
     if ((st = status_word(&status)) != NVFP4_OK) return st;
 
     // few activation rows: the swapped-operand kernel (gemm_small.cu)
-    if constexpr (ACT) {
-        if (M <= kSmallMaxRows)
-            return launch_gemm_small_act(a, sfa, b, sfb, I8, RSB, alpha, sx, sw, bias, *epi, y, M,
-                                         N, K, stream, weights_ready);
-    } else if constexpr (!QOUT && !I8) {
+    if constexpr (!QOUT && !I8) {
         if (M <= kSmallMaxRows)
             return launch_gemm_small(a, sfa, b, sfb, RSB, F32, alpha, bias, y, M, N, K, stream,
                                      weights_ready);
     }
     const int64_t kbytes = I8 ? K : K / 2;   // bytes of one operand row
-    CUtensorMap mapA, mapB, mapY, mapR;
+    CUtensorMap mapA, mapB, mapY;
     if (!make_operand_map(&mapA, a, M, kbytes, BM) || !make_operand_map(&mapB, b, N, kbytes, BN))
         return NVFP4_ERR_CUDA;
-    const bool gated = ACT && (epi->activation & NVFP4_ACT_GATED);
-    const int64_t n_out = gated ? N / 2 : N;
-    const bool tma_store = !QOUT && !F32 && (n_out % 8) == 0;
+    const bool tma_store = !QOUT && !F32 && (N % 8) == 0;
     if (tma_store) {
-        if (!make_output_map(&mapY, y, M, n_out)) return NVFP4_ERR_CUDA;
+        if (!make_output_map(&mapY, y, M, N)) return NVFP4_ERR_CUDA;
     } else {
         mapY = mapA;   // unused
     }
-    mapR = mapY;       // unused without a residual
-    if (ACT && tma_store && epi->residual &&
-        !make_output_map(&mapR, const_cast<void*>(epi->residual), M, n_out))
-        return NVFP4_ERR_CUDA;
 
     static std::atomic<int> attr_set[64];
     if (!attr_set[dev.device & 63].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(gemm_kernel<QOUT, I8, false, RSB, F32, ACT>,
+        if (cudaFuncSetAttribute(gemm_kernel<QOUT, I8, false, RSB, F32>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 GemmSmem<RSB, ACT>::BYTES) != cudaSuccess)
+                                 GemmSmem<RSB>::BYTES) != cudaSuccess)
             return NVFP4_ERR_CUDA;
         attr_set[dev.device & 63].store(1, std::memory_order_release);
     }
@@ -1039,24 +838,17 @@ nvfp4_status launch_gemm_impl(const uint8_t* a, const uint8_t* sfa, const uint8_
         p.q_gsf = q->gsf;
         p.q_cgroups = (int)(N / 64);
     }
-    if (ACT) {
-        p.act = epi->activation;
-        p.gated = gated ? 1 : 0;
-        p.n_out = (int)n_out;
-        p.residual = static_cast<const uint16_t*>(epi->residual);
-    }
     p.w_early = weights_ready ? 1 : 0;
     p.status = status;
     p.budget_ns = 4000000000ull;   // 4 s
 
     const int tiles = p.m_blocks * p.n_blocks;
-    if constexpr (!QOUT && (!I8 || ACT)) {
+    if constexpr (!QOUT && !I8) {
 
-        const int splits = choose_splits<I8, RSB, F32, ACT>(tiles, p.k_tiles, dev);
+        const int splits = choose_splits<false, RSB, F32, false>(tiles, p.k_tiles, dev);
         if (splits > 1) {
             p.splits = splits;
-            return launch_split_k<I8, RSB, F32, ACT>(mapA, mapB, mapY, mapR, p, tiles * splits,
-                                                     splits, stream);
+            return launch_split_k<false, RSB, F32, false>(mapA, mapB, mapY, p, tiles * splits, splits, stream);
         }
         // One full wave plus a short second one (at most SMs / 2 tiles) of long tiles
         // (K >= 4096): the full wave runs persistent, the leftover tiles split K over
@@ -1065,26 +857,24 @@ nvfp4_status launch_gemm_impl(const uint8_t* a, const uint8_t* sfa, const uint8_
         // it replaces only the last of many waves or a short-K wave.
         const int tail = tiles % dev.sms;
         if (tiles > dev.sms && tiles < 2 * dev.sms && tail > 0 && p.k_tiles >= 16) {
-            const int ts = choose_splits<I8, RSB, F32, ACT>(tail, p.k_tiles, dev);
+            const int ts = choose_splits<false, RSB, F32, false>(tail, p.k_tiles, dev);
             if (ts > 1) {
                 GemmParams full = p;
                 full.tile_count = tiles - tail;
-                if (launch_pdl(gemm_kernel<false, I8, false, RSB, F32, ACT>, (unsigned)dev.sms,
-                               THREADS, GemmSmem<RSB, ACT>::BYTES, stream, mapA, mapB, mapY, mapR,
-                               full) != cudaSuccess)
+                if (launch_pdl(gemm_kernel<false, false, false, RSB, F32>, (unsigned)dev.sms, THREADS,
+                               GemmSmem<RSB>::BYTES, stream, mapA, mapB, mapY, full) != cudaSuccess)
                     return NVFP4_ERR_CUDA;
                 GemmParams rest = p;
                 rest.tile_base = tiles - tail;
                 rest.tile_count = tail;
                 rest.splits = ts;
-                return launch_split_k<I8, RSB, F32, ACT>(mapA, mapB, mapY, mapR, rest, tail * ts, ts,
-                                                         stream);
+                return launch_split_k<false, RSB, F32, false>(mapA, mapB, mapY, rest, tail * ts, ts, stream);
             }
         }
     }
     const int grid = tiles < dev.sms ? tiles : dev.sms;
-    if (launch_pdl(gemm_kernel<QOUT, I8, false, RSB, F32, ACT>, (unsigned)grid, THREADS,
-                   GemmSmem<RSB, ACT>::BYTES, stream, mapA, mapB, mapY, mapR, p) != cudaSuccess)
+    if (launch_pdl(gemm_kernel<QOUT, I8, false, RSB, F32>, (unsigned)grid, THREADS,
+                   GemmSmem<RSB>::BYTES, stream, mapA, mapB, mapY, p) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     return NVFP4_OK;
 }
@@ -1169,33 +959,68 @@ nvfp4_status launch_gemm_quant_out(const uint8_t* a, const uint8_t* sfa, const u
                                          nullptr, nullptr, stream);
 }
 
-nvfp4_status launch_gemm_act(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
-                             const uint8_t* sfb, bool sfb_prepared, const float* alpha,
-                             const void* bias, const EpilogueArgs& epi, void* y, int64_t M,
-                             int64_t N, int64_t K, cudaStream_t stream, bool weights_ready) {
-    if (sfb_prepared)
-        return launch_gemm_impl<false, false, true, false, true>(
-            a, sfa, b, sfb, alpha, bias, y, M, N, K, nullptr, nullptr, nullptr, stream,
-            weights_ready, &epi);
-    return launch_gemm_impl<false, false, false, false, true>(a, sfa, b, sfb, alpha, bias, y, M, N,
-                                                              K, nullptr, nullptr, nullptr, stream,
-                                                              weights_ready, &epi);
-}
-
-nvfp4_status launch_int8_gemm_act(const int8_t* a, const float* sa, const int8_t* b,
-                                  const float* sb, const void* bias, const EpilogueArgs& epi,
-                                  void* y, int64_t M, int64_t N, int64_t K, cudaStream_t stream) {
-    return launch_gemm_impl<false, true, false, false, true>(
-        reinterpret_cast<const uint8_t*>(a), nullptr, reinterpret_cast<const uint8_t*>(b), nullptr,
-        nullptr, bias, y, M, N, K, nullptr, sa, sb, stream, false, &epi);
-}
-
 nvfp4_status launch_int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const float* sb,
                               const void* bias, void* y, int64_t M, int64_t N, int64_t K,
                               cudaStream_t stream) {
     return launch_gemm_impl<false, true>(reinterpret_cast<const uint8_t*>(a), nullptr,
                                          reinterpret_cast<const uint8_t*>(b), nullptr, nullptr,
                                          bias, y, M, N, K, nullptr, sa, sb, stream);
+}
+
+namespace {
+
+template <bool I8, bool RSB>
+nvfp4_status gemm_act_split_k(const GemmActArgs& g, bool* taken, cudaStream_t stream) {
+    *taken = false;
+    DeviceInfo dev;
+    nvfp4_status st = device_info(&dev);
+    if (st != NVFP4_OK) return st;
+    const int64_t kbytes = I8 ? g.K : g.K / 2;
+    const int64_t m_blocks = (g.M + BM - 1) / BM, n_blocks = (g.N + BN - 1) / BN;
+    if (m_blocks * n_blocks * 2 > dev.sms) return NVFP4_OK;
+    const int tiles = (int)(m_blocks * n_blocks), k_tiles = (int)((kbytes + BKB - 1) / BKB);
+    const int splits = choose_splits<I8, RSB, false, true>(tiles, k_tiles, dev);
+    if (splits < 2) return NVFP4_OK;
+    *taken = true;
+    int* status = nullptr;
+    if ((st = status_word(&status)) != NVFP4_OK) return st;
+    CUtensorMap mapA, mapB;
+    if (!make_operand_map(&mapA, g.a, g.M, kbytes, BM) || !make_operand_map(&mapB, g.b, g.N, kbytes, BN))
+        return NVFP4_ERR_CUDA;
+    GemmParams p{};
+    p.sfa = g.sfa;
+    p.sfb = g.sfb;
+    p.alpha = g.alpha;
+    p.sx = g.sx;
+    p.sw = g.sw;
+    p.bias = static_cast<const uint16_t*>(g.bias);
+    p.y = static_cast<uint16_t*>(g.y);
+    p.M = (int)g.M;
+    p.N = (int)g.N;
+    p.m_blocks = (int)m_blocks;
+    p.n_blocks = (int)n_blocks;
+    p.k_tiles = k_tiles;
+    p.kchunks = (int)(kbytes / 32);
+    p.sf_row_tiles_b = (int)((g.N + 127) / 128);
+    p.n_fast = g.N <= g.M ? 1 : 0;
+    p.splits = splits;
+    p.tile_count = tiles;
+    p.act = g.epi.activation;
+    p.gated = (g.epi.activation & NVFP4_ACT_GATED) ? 1 : 0;
+    p.n_out = (int)(p.gated ? g.N / 2 : g.N);
+    p.residual = static_cast<const uint16_t*>(g.epi.residual);
+    p.w_early = g.weights_ready ? 1 : 0;
+    p.status = status;
+    p.budget_ns = 4000000000ull;   // 4 s
+    return launch_split_k<I8, RSB, false, true>(mapA, mapB, mapA, p, tiles * splits, splits, stream);
+}
+
+}  // namespace
+
+nvfp4_status launch_gemm_act_split_k(const GemmActArgs& g, bool* taken, cudaStream_t stream) {
+    if (g.int8) return gemm_act_split_k<true, false>(g, taken, stream);
+    return g.sfb_prepared ? gemm_act_split_k<false, true>(g, taken, stream)
+                          : gemm_act_split_k<false, false>(g, taken, stream);
 }
 
 }  // namespace nvfp4

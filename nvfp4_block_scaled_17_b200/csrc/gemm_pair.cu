@@ -1,0 +1,676 @@
+// gemm_pair.cu -- the products with an activation and a residual in their epilogue, for
+// grids that fill the GPU: two SMs on one 256 x 256 output tile.
+//
+//     v = fp32(scale * acc) + bias;  u = act(v), or act(v[2j]) v[2j + 1];  y = bf16(u + r)
+//
+// Why pairs.  An SM's shared memory moves 128 bytes a cycle.  A 128 x 256 tile on one SM
+// reads 12 KiB per 128-cycle MMA (4 KiB of A, 8 KiB of B) and takes the same 12 KiB in from
+// TMA: 192 bytes a cycle, so such a kernel runs the tensor cores at two thirds.  With
+// cta_group::2 each SM holds 128 rows of A and 128 of B, and the pair shares B: 8 KiB read
+// and 8 KiB written per MMA, 128 bytes a cycle; the traffic from L2 falls by a third too.
+//
+// Design (a cluster of two CTAs, persistent over tiles; 576 threads each):
+//   warp 0      TMA producer of its CTA: per stage (128 bytes of K) a 128-row A box, a
+//               128-row B box (128-byte swizzle) and, for FP4, the scale chunks of its own
+//               A rows and of all 256 B rows, which each SM needs in its tensor memory.
+//               Every load signals the leader's full barrier (cta_group::2 loads may).
+//   warp 1      in the leader: MMA issue for both SMs (M = 256, N = 256), the whole warp
+//               converged, one election per K step; commits arrive at both CTAs' barriers.
+//   warps 2-17  epilogue of the CTA's 128 rows: four warps per tensor-memory quadrant, each
+//               64 columns wide, which it reads into 64 registers at once.  So the
+//               accumulator is released as soon as it has been read, before any of it is
+//               scaled, activated or stored, and the next tile's MMAs overlap all of that.
+//               Output chunks of 32 x 32 go through a swizzled staging tile and a TMA store;
+//               with a residual, its chunk is loaded into the same staging tile a tile ahead.
+// int8 accumulators are two full 256-column buffers; FP4 ones share 64 columns ([0, 256) and
+// [192, 448)) to leave room for the scale ring at [448, 508).
+//
+// Every wait is bounded; on expiry the kernel records NVFP4_ERR_TIMEOUT, lets its copies
+// land, frees tensor memory and returns.  No load uses cluster multicast.
+#include "activation.cuh"
+#include "common.cuh"
+#include "kernels.h"
+
+#include <atomic>
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int PROWS = 128;                    // A rows, and B rows, of one CTA
+constexpr int PN = 256;                       // columns of a tile
+constexpr int PKB = 128;                      // bytes of K per stage
+constexpr int PSTAGES = 4;
+constexpr int PEPI = 16;                      // epilogue warps
+constexpr int PTHREADS = 64 + 32 * PEPI;
+constexpr int PS_OP = PROWS * PKB;            // 16 KiB: A, and B
+constexpr int PS_SFA = 4 * 512;
+constexpr int PS_SFB = 8 * 512;
+constexpr int P_STG = 32 * 64;                // one 32 x 32 bf16 staging tile; two per warp
+constexpr int P_COLS = 64 * 4 + 64 * 2;       // a warp's column scales (int8) and bias
+template <bool I8>
+struct PairSmem {
+    static constexpr int STAGE = 2 * PS_OP + (I8 ? 0 : PS_SFA + PS_SFB);
+    static constexpr int BYTES = 1024 + PSTAGES * STAGE + PEPI * (2 * P_STG + P_COLS) + 512;
+};
+static_assert(PairSmem<false>::BYTES <= 232448 && PairSmem<true>::BYTES <= 232448,
+              "dynamic shared memory above the 227 KiB a CTA can have");
+constexpr uint32_t PTMEM_SF = 448;
+constexpr int PSF_SLOTS = 5;
+// E2M1 x E2M1 (format 1), or signed int8 (format 1) with an int32 accumulator; K-major,
+// N = 256, M = 256 over the pair
+constexpr uint32_t PIDESC = (1u << 7) | (1u << 10) | ((uint32_t)(PN >> 3) << 17) | (16u << 24);
+constexpr uint32_t PIDESC_I8 = PIDESC | (2u << 4);
+
+struct PairParams {
+    const float* alpha;
+    const float* sx;           // int8: fp32 row scales of A and of B
+    const float* sw;
+    const uint16_t* bias;      // bf16 [N] or null
+    const uint16_t* residual;  // bf16 [M, n_out] or null
+    uint16_t* y;               // bf16 [M, n_out]
+    int M, N, n_out;
+    int act, gated;
+    int m_blocks, n_blocks, tiles;
+    int k_tiles;               // stages of K
+    int kchunks;               // 32-byte K steps
+    int prepared;              // B scales: 1 = prepared blocks, 0 = 128x4 chunks
+    int n_fast;
+    int tma_store;             // n_out % 8 == 0
+    int w_early;               // B was complete before the previous kernel started
+    int* status;
+    uint64_t budget_ns;
+};
+
+// ---- cta_group::2 forms -------------------------------------------------------------------
+
+__device__ __forceinline__ void tma_load_2d_pair_w(uint32_t dst, const CUtensorMap* map,
+                                                   uint32_t leader_bar, int32_t x, int32_t y) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(leader_bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+// Completion of all earlier MMAs and scale copies, to the barrier at this offset in both CTAs.
+__device__ __forceinline__ void commit_both_w(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+        ".b64 [%0], m;\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void commit_own_w(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void pair_step_i8_w(uint32_t d, uint64_t ad, uint64_t bd,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(PIDESC_I8), "r"(accumulate)
+        : "memory");
+}
+
+// One FP4 K step: each SM's scale chunks (its A rows; both halves of B) from its own shared
+// memory into its own tensor memory, then the MMA over both.
+__device__ __forceinline__ void pair_step_fp4_w(uint32_t d, uint64_t ad, uint64_t bd, uint32_t sf_t,
+                                                uint64_t sfa_d, uint64_t sfb_d,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 t, u;\n\t.reg .b64 s;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "add.u32 t, %5, 4;\n\t"
+        "add.u32 u, %5, 8;\n\t"
+        "add.u64 s, %7, 128;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%5], %6;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t], %7;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [u], s;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], "
+        "[t], p;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(PIDESC), "r"(accumulate), "r"(sf_t), "l"(sfa_d), "l"(sfb_d)
+        : "memory");
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// The bounded wait of common.cuh for arrivals that come from the other CTA as well.
+__device__ __forceinline__ bool wait_cluster_w(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                               int* status, uint64_t budget_ns) {
+    auto ready = [&]() {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        return ok != 0;
+    };
+    bool ok = ready();
+    if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!(ok = ready())) {
+            if (*abort) break;
+            if (globaltimer_ns() - t0 > budget_ns) {
+                record_status(status, NVFP4_ERR_TIMEOUT);
+                *abort = 1;
+                break;
+            }
+        }
+    }
+    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+__device__ __forceinline__ void pair_coords(const PairParams& p, int tile, int& m_blk, int& n_blk) {
+    if (p.n_fast) {
+        m_blk = tile / p.n_blocks;
+        n_blk = tile - m_blk * p.n_blocks;
+    } else {
+        n_blk = tile / p.m_blocks;
+        m_blk = tile - n_blk * p.m_blocks;
+    }
+}
+
+template <bool I8>
+__global__ void __launch_bounds__(PTHREADS, 1)
+gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
+                 const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmR,
+                 const PairParams p) {
+    using SM = PairSmem<I8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    uint8_t* sStg = smem + PSTAGES * SM::STAGE;
+    uint8_t* sCols = sStg + PEPI * 2 * P_STG;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sCols + PEPI * P_COLS);   // used in the leader
+    uint64_t* empty = full + PSTAGES;
+    uint64_t* acc_full = empty + PSTAGES;    // [2]
+    uint64_t* acc_free = acc_full + 2;       // [2], used in the leader
+    uint64_t* ovl_free = acc_free + 2;       // used in the leader
+    uint64_t* drain = ovl_free + 1;
+    uint64_t* res_full = drain + 1;          // [PEPI][2]
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(res_full + 2 * PEPI);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < PSTAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_free[b], 2 * PEPI);
+        }
+        mbar_init(ovl_free, 2 * PEPI / 4);
+        mbar_init(drain, 1);
+        for (int s = 0; s < 2 * PEPI; ++s) mbar_init(&res_full[s], 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+            smem_u32(tmem_holder)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();          // both CTAs' barriers and tensor memory exist
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+
+    // Producer: one stage's B side (box and scales) and A side.
+    const uint32_t full0 = dsmem_addr(smem_u32(full), 0);    // the leader's full barriers
+    auto load_b = [&](int stage, int kt, int n_blk) {
+        const uint32_t s = smem_u32(smem + stage * SM::STAGE), bar = full0 + 8u * (uint32_t)stage;
+        tma_load_2d_pair_w(s + PS_OP, &tmB, bar, kt * PKB, n_blk * PN + rank * PROWS);
+        if constexpr (!I8) {
+            // 512-byte scale chunks of the tile's two 128-row halves, four K steps each
+            const int at = p.prepared ? (n_blk * p.k_tiles + kt) * 8 : 2 * n_blk * p.kchunks + 4 * kt;
+            const int second = p.prepared ? 4 : p.kchunks;
+            tma_load_2d_pair_w(s + 2 * PS_OP + PS_SFA, &tmSFB, bar, 0, at);
+            tma_load_2d_pair_w(s + 2 * PS_OP + PS_SFA + 2048, &tmSFB, bar, 0, at + second);
+        }
+    };
+    auto load_a = [&](int stage, int kt, int m_blk) {
+        const uint32_t s = smem_u32(smem + stage * SM::STAGE), bar = full0 + 8u * (uint32_t)stage;
+        tma_load_2d_pair_w(s, &tmA, bar, kt * PKB, m_blk * 2 * PROWS + rank * PROWS);
+        if constexpr (!I8)
+            tma_load_2d_pair_w(s + 2 * PS_OP, &tmSFA, bar, 0, (2 * m_blk + rank) * p.kchunks + 4 * kt);
+    };
+    int n_early = 0;
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_tensormap(&tmA);
+            prefetch_tensormap(&tmB);
+        }
+        if (p.w_early && pair < p.tiles) {
+            int m_blk, n_blk;
+            pair_coords(p, pair, m_blk, n_blk);
+            n_early = min(PSTAGES, p.k_tiles);
+            for (int i = 0; i < n_early; ++i) {
+                if (rank == 0) mbar_arrive_expect_tx_w(&full[i], 2 * SM::STAGE);
+                load_b(i, i, n_blk);
+            }
+        }
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+
+    if (warp == 0) {
+        int stage = 0, fills = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = pair; ok && tile < p.tiles; tile += pairs) {
+            int m_blk, n_blk;
+            pair_coords(p, tile, m_blk, n_blk);
+            for (int kt = 0; kt < p.k_tiles; ++kt, ++fills) {
+                if (fills >= n_early) {
+                    if (!mbar_wait_bounded_warp(&empty[stage], phase ^ 1, abort_flag, p.status,
+                                                p.budget_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx_w(&full[stage], 2 * SM::STAGE);
+                    load_b(stage, kt, n_blk);
+                }
+                load_a(stage, kt, m_blk);
+                if (++stage == PSTAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        // Every fill is consumed by an MMA before the epilogue ends; only after a wait that
+        // ran out can copies still be on their way, and they land within microseconds.
+        if (!ok) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 2000000) {}
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            int stage = 0, it = 0, sf_slot = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int tile = pair; ok && tile < p.tiles; tile += pairs, ++it) {
+                const int b = it & 1;
+                const uint32_t use = (uint32_t)(it >> 1);
+                if (!wait_cluster_w(&acc_free[b], (use & 1) ^ 1, abort_flag, p.status, p.budget_ns) ||
+                    (!I8 && !wait_cluster_w(ovl_free, (uint32_t)(it & 1) ^ 1, abort_flag, p.status,
+                                            p.budget_ns))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t acc = tmem + (b ? (I8 ? 256u : 192u) : 0u);
+                for (int kt = 0; kt < p.k_tiles; ++kt) {
+                    if (!wait_cluster_w(&full[stage], phase, abort_flag, p.status, p.budget_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int steps = min(4, p.kchunks - 4 * kt);
+                    const uint32_t s = smem_u32(smem + stage * SM::STAGE);
+                    const uint64_t ad = sdesc_kmajor_sw128(s), bd = sdesc_kmajor_sw128(s + PS_OP);
+                    const uint64_t sad = sdesc_sf(s + 2 * PS_OP), sbd = sdesc_sf(s + 2 * PS_OP + PS_SFA);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk < steps) {
+                            const uint32_t accumulate = (kt > 0 || kk > 0) ? 1u : 0u;
+                            if constexpr (I8) {
+                                pair_step_i8_w(acc, ad + 2 * kk, bd + 2 * kk, accumulate);
+                            } else {
+                                pair_step_fp4_w(acc, ad + 2 * kk, bd + 2 * kk,
+                                                tmem + PTMEM_SF + 12u * (uint32_t)sf_slot,
+                                                sad + 32 * kk, sbd + 32 * kk, accumulate);
+                                sf_slot = sf_slot == PSF_SLOTS - 1 ? 0 : sf_slot + 1;
+                            }
+                        }
+                    }
+                    commit_both_w(&empty[stage]);
+                    if (++stage == PSTAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                commit_both_w(&acc_full[b]);
+            }
+            // every tensor-core operation of the pair has finished
+            commit_own_w(drain);
+            volatile int no_abort = 0;
+            mbar_wait_bounded(drain, 0, &no_abort, p.status, p.budget_ns);
+        }
+        __syncwarp();
+    } else {
+        const int e = warp - 2;
+        const int quad = warp & 3;               // tensor-memory lanes 32 quad .. + 31
+        const int quarter = e >> 2;              // columns 64 quarter .. + 63
+        uint8_t* stg = sStg + e * 2 * P_STG;
+        float* ssw = reinterpret_cast<float*>(sCols + e * P_COLS);
+        uint32_t* sbias = reinterpret_cast<uint32_t*>(sCols + e * P_COLS + 256);
+        uint64_t* rfull = res_full + 2 * e;
+        const uint32_t free0 = dsmem_addr(smem_u32(acc_free), 0);
+        const uint32_t ovl0 = dsmem_addr(smem_u32(ovl_free), 0);
+        const float alpha = I8 ? 0.0f : *p.alpha;
+        const bool gated = p.gated != 0;
+        const bool res_tma = p.residual && p.tma_store;
+        uint32_t res_phase = 0, res_ahead = 0;   // per staging tile: parity; loaded, not used
+        // Loads the residual chunks of `tile` into the staging tiles that its output will take:
+        // chunk c in staging tile c (one chunk when gated).
+        auto load_residual = [&](int tile) {
+            if (tile >= p.tiles) return;
+            int m_blk, n_blk;
+            pair_coords(p, tile, m_blk, n_blk);
+            const int row = m_blk * 2 * PROWS + rank * PROWS + quad * 32;
+            const int n0 = n_blk * PN + quarter * 64;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int col = gated ? n0 >> 1 : n0 + 32 * c;
+                if ((gated && c) || col >= p.n_out) continue;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&rfull[c], P_STG);
+                    tma_load_2d(stg + c * P_STG, &tmR, &rfull[c], col, row);
+                }
+                res_ahead |= 1u << c;
+            }
+        };
+        if (res_tma) load_residual(pair);
+        int it = 0;
+        bool ok = true;
+        for (int tile = pair; ok && tile < p.tiles; tile += pairs, ++it) {
+            int m_blk, n_blk;
+            pair_coords(p, tile, m_blk, n_blk);
+            const int b = it & 1;
+            const uint32_t use = (uint32_t)(it >> 1);
+            const int row0 = m_blk * 2 * PROWS + rank * PROWS + quad * 32;
+            const int n0 = n_blk * PN + quarter * 64;
+            // this warp's column values, before the accumulator wait (columns past N repeat
+            // the last one; they are not stored)
+            const int n = n0 + 2 * lane;
+            float2 sw2 = make_float2(0.0f, 0.0f);
+            uint32_t bias2 = 0u;
+            if (I8) {
+                if (n + 2 <= p.N) sw2 = *reinterpret_cast<const float2*>(p.sw + n);
+                else sw2 = make_float2(p.sw[min(n, p.N - 1)], p.sw[min(n + 1, p.N - 1)]);
+            }
+            if (p.bias) {
+                if (n + 2 <= p.N) bias2 = *reinterpret_cast<const uint32_t*>(p.bias + n);
+                else bias2 = (uint32_t)p.bias[min(n, p.N - 1)] | ((uint32_t)p.bias[min(n + 1, p.N - 1)] << 16);
+            }
+            const float scale = I8 ? (row0 + lane < p.M ? p.sx[row0 + lane] : 0.0f) : alpha;
+            __syncwarp();                        // the last tile's values have been read
+            if (I8) reinterpret_cast<float2*>(ssw)[lane] = sw2;
+            sbias[lane] = bias2;
+            __syncwarp();
+            if (!mbar_wait_bounded_warp(&acc_full[b], use & 1, abort_flag, p.status, p.budget_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t r0[32], r1[32];
+            const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + (b ? (I8 ? 256u : 192u) : 0u) +
+                                (uint32_t)(quarter * 64);
+            tmem_ld32(at, r0);
+            tmem_ld32(at + 32, r1);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                // buffer 0's last quarter and buffer 1's first are the shared columns
+                if (!I8 && quarter == (b ? 0 : 3)) arrive_cluster(ovl0);
+                arrive_cluster(free0 + 8u * (uint32_t)b);
+            }
+
+            auto values = [&](uint32_t (&r)[32], int c) {
+                float v[32];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    if constexpr (I8) {
+                        const float4 s4 = reinterpret_cast<const float4*>(ssw)[8 * c + q];
+                        v[4 * q] = __fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * q]), scale), s4.x);
+                        v[4 * q + 1] = __fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * q + 1]), scale), s4.y);
+                        v[4 * q + 2] = __fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * q + 2]), scale), s4.z);
+                        v[4 * q + 3] = __fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * q + 3]), scale), s4.w);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[4 * q + j] = __fmul_rn(scale, __uint_as_float(r[4 * q + j]));
+                    }
+                }
+                if (p.bias) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 w = reinterpret_cast<const uint4*>(sbias)[4 * c + q];
+                        const uint32_t bw[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            v[8 * q + 2 * j] = __fadd_rn(v[8 * q + 2 * j], bf16lo(bw[j]));
+                            v[8 * q + 2 * j + 1] = __fadd_rn(v[8 * q + 2 * j + 1], bf16hi(bw[j]));
+                        }
+                    }
+                }
+                apply_activation(v, p.act, gated);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(v[j]);
+            };
+            // One output chunk u(0) .. u(31) at column col: residual, rounding, store.
+            auto store = [&](auto u, int s, int col) -> bool {
+                if (!p.tma_store) {
+                    const int row = row0 + lane;
+                    if (row < p.M) {
+                        const size_t o = (size_t)row * p.n_out + col;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (col + j < p.n_out) {
+                                float t = u(j);
+                                if (p.residual)
+                                    t = __fadd_rn(t, __uint_as_float((uint32_t)p.residual[o + j] << 16));
+                                p.y[o + j] = (uint16_t)bf16x2_rn(t, 0.0f);
+                            }
+                    }
+                    return true;
+                }
+                uint8_t* sb = stg + s * P_STG;
+                if (res_tma) {
+                    if (!mbar_wait_bounded_warp(&rfull[s], (res_phase >> s) & 1, abort_flag, p.status,
+                                                p.budget_ns))
+                        return false;
+                    res_phase ^= 1u << s;
+                    res_ahead &= ~(1u << s);
+                }
+                // 64-byte swizzle: 16-byte chunk c of row r sits at c ^ ((r >> 1) & 3)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint4* o = reinterpret_cast<uint4*>(sb + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+                    uint32_t w[4];
+                    if (res_tma) {
+                        const uint4 t = *o;
+                        const uint32_t rw[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = bf16x2_rn(__fadd_rn(u(8 * c + 2 * j), bf16lo(rw[j])),
+                                             __fadd_rn(u(8 * c + 2 * j + 1), bf16hi(rw[j])));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[j] = bf16x2_rn(u(8 * c + 2 * j), u(8 * c + 2 * j + 1));
+                    }
+                    *o = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&tmY, sb, col, row0);
+                    bulk_commit();
+                }
+                return true;
+            };
+            // A staging tile is free when the last tile's stores have read it; with a
+            // residual that was waited for before the residual was loaded.
+            if (!res_tma && p.tma_store) {
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
+            }
+            if (n0 < p.N) values(r0, 0);         // warp-uniform, here and below
+            if (n0 >= p.N) {
+            } else if (gated) {
+                if (n0 + 32 < p.N) values(r1, 1);
+                ok = store([&](int j) {
+                    return __uint_as_float(j < 16 ? r0[2 * (j & 15)] : r1[2 * (j & 15)]);
+                }, 0, n0 >> 1);
+            } else {
+                ok = store([&](int j) { return __uint_as_float(r0[j]); }, 0, n0);
+                if (ok && n0 + 32 < p.N) {
+                    values(r1, 1);
+                    ok = store([&](int j) { return __uint_as_float(r1[j]); }, 1, n0 + 32);
+                }
+            }
+            if (ok && res_tma) {
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
+                load_residual(tile + pairs);
+            }
+        }
+        // residual chunks still on their way must land before the block can exit
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            if (res_ahead & (1u << s)) {
+                volatile int no_abort = 0;
+                mbar_wait_bounded(&rfull[s], (res_phase >> s) & 1, &no_abort, p.status, p.budget_ns);
+            }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+
+    // Every thread gets here after bounded work.  The barrier keeps both CTAs' shared and
+    // tensor memory alive until neither is used by the other.
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+// 512-byte scale chunks as the rows of a 2-D tensor of 32-bit words, four rows per load.
+bool make_scale_map(CUtensorMap* map, const void* base, int64_t chunks) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {128, (cuuint64_t)chunks};
+    cuuint64_t strides[1] = {512};
+    cuuint32_t box[2] = {128, 4};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool I8>
+nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
+    DeviceInfo dev;
+    nvfp4_status st = device_info(&dev);
+    if (st != NVFP4_OK) return st;
+    int* status = nullptr;
+    if ((st = status_word(&status)) != NVFP4_OK) return st;
+    static std::atomic<int> attr_set[64];
+    if (!attr_set[dev.device & 63].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(gemm_pair_kernel<I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 PairSmem<I8>::BYTES) != cudaSuccess)
+            return NVFP4_ERR_CUDA;
+        attr_set[dev.device & 63].store(1, std::memory_order_release);
+    }
+    PairParams p{};
+    const int64_t kbytes = I8 ? g.K : g.K / 2;
+    p.alpha = g.alpha;
+    p.sx = g.sx;
+    p.sw = g.sw;
+    p.bias = static_cast<const uint16_t*>(g.bias);
+    p.residual = static_cast<const uint16_t*>(g.epi.residual);
+    p.y = static_cast<uint16_t*>(g.y);
+    p.M = (int)g.M;
+    p.N = (int)g.N;
+    p.act = g.epi.activation;
+    p.gated = (g.epi.activation & NVFP4_ACT_GATED) ? 1 : 0;
+    p.n_out = (int)(p.gated ? g.N / 2 : g.N);
+    p.m_blocks = (int)((g.M + 2 * PROWS - 1) / (2 * PROWS));
+    p.n_blocks = (int)((g.N + PN - 1) / PN);
+    p.tiles = p.m_blocks * p.n_blocks;
+    p.k_tiles = (int)((kbytes + PKB - 1) / PKB);
+    p.kchunks = (int)(kbytes / 32);
+    p.prepared = g.sfb_prepared ? 1 : 0;
+    p.n_fast = g.N <= g.M ? 1 : 0;
+    p.tma_store = p.n_out % 8 == 0;
+    p.w_early = g.weights_ready ? 1 : 0;
+    p.status = status;
+    p.budget_ns = 4000000000ull;   // 4 s
+    CUtensorMap mapA, mapB, mapSFA, mapSFB, mapY, mapR;
+    if (!make_operand_map(&mapA, g.a, g.M, kbytes, PROWS) ||
+        !make_operand_map(&mapB, g.b, g.N, kbytes, PROWS))
+        return NVFP4_ERR_CUDA;
+    mapSFA = mapSFB = mapY = mapA;             // where unused
+    if (!I8) {
+        const int64_t b_chunks = p.prepared ? (int64_t)p.n_blocks * p.k_tiles * 8
+                                            : (g.N + 127) / 128 * p.kchunks;
+        if (!make_scale_map(&mapSFA, g.sfa, (g.M + 127) / 128 * p.kchunks) ||
+            !make_scale_map(&mapSFB, g.sfb, b_chunks))
+            return NVFP4_ERR_CUDA;
+    }
+    if (p.tma_store && !make_output_map(&mapY, g.y, g.M, p.n_out)) return NVFP4_ERR_CUDA;
+    mapR = mapY;
+    if (p.tma_store && p.residual &&
+        !make_output_map(&mapR, const_cast<void*>(g.epi.residual), g.M, p.n_out))
+        return NVFP4_ERR_CUDA;
+
+    const int pairs = p.tiles < dev.sms / 2 ? p.tiles : dev.sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
+    cfg.blockDim = dim3(PTHREADS, 1, 1);
+    cfg.dynamicSmemBytes = PairSmem<I8>::BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<I8>, mapA, mapB, mapSFA, mapSFB, mapY, mapR, p) ==
+                   cudaSuccess
+               ? NVFP4_OK
+               : NVFP4_ERR_CUDA;
+}
+
+}  // namespace
+
+nvfp4_status launch_gemm_act(const GemmActArgs& g, cudaStream_t stream) {
+    if (g.M <= kSmallMaxRows) return launch_gemm_small_act(g, stream);
+    bool taken = false;
+    const nvfp4_status st = launch_gemm_act_split_k(g, &taken, stream);
+    if (st != NVFP4_OK || taken) return st;
+    return g.int8 ? launch_pair_impl<true>(g, stream) : launch_pair_impl<false>(g, stream);
+}
+
+}  // namespace nvfp4

@@ -379,24 +379,10 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
             const int n = tile * XW_ROWS + 4 * g;
             if (n >= p.N) continue;
             const uint32_t off = part + (uint32_t)((m * XW_ROWS + 4 * g) * 4);
-            if constexpr (I8) {   // integer partial sums: exact in any order
-                int acc[4] = {0, 0, 0, 0};
-                for (int r = 0; r < splits; ++r) {
-                    const float4 t = ld_dsmem_f4(dsmem_addr(off, (uint32_t)r));
-                    acc[0] += __float_as_int(t.x);
-                    acc[1] += __float_as_int(t.y);
-                    acc[2] += __float_as_int(t.z);
-                    acc[3] += __float_as_int(t.w);
-                }
-                const float sx = p.sx[m];
-                float v[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[j] = __fmul_rn(__fmul_rn(__int2float_rn(acc[j]), sx), p.sw[min(n + j, p.N - 1)]);
-                    if (p.bias)
-                        v[j] = __fadd_rn(v[j], __uint_as_float((uint32_t)p.bias[min(n + j, p.N - 1)] << 16));
-                }
-                finish_granule(v, p.act, p.gated != 0, p.residual, p.y, m, n, p.n_out);
+            if constexpr (ACT) {
+                float u[4];
+                reduce_granule<I8>(u, off, splits, alpha, I8 ? p.sx[m] : 0.0f, p.sw, p.bias, n, p.N);
+                finish_granule(u, p.act, p.gated != 0, p.residual, p.y, m, n, p.n_out);
                 continue;
             }
             float4 acc = ld_dsmem_f4(dsmem_addr(off, 0));
@@ -414,9 +400,7 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 for (int j = 0; j < 4; ++j)
                     v[j] = __fadd_rn(v[j], __uint_as_float((uint32_t)p.bias[min(n + j, p.N - 1)] << 16));
             }
-            if constexpr (ACT) {
-                finish_granule(v, p.act, p.gated != 0, p.residual, p.y, m, n, p.n_out);
-            } else if constexpr (F32) {
+            if constexpr (F32) {
                 float* yp = p.y32 + (size_t)m * p.N + n;
                 for (int j = 0; j < 4 && n + j < p.N; ++j) yp[j] = v[j];
             } else {
@@ -561,20 +545,15 @@ nvfp4_status launch_gemm_small(const uint8_t* a, const uint8_t* sfa, const uint8
                    : launch_small_impl<false, false>(a, sfa, b, sfb, alpha, bias, y, M, N, K, stream, w);
 }
 
-nvfp4_status launch_gemm_small_act(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
-                                   const uint8_t* sfb, bool int8, bool sfb_prepared,
-                                   const float* alpha, const float* sx, const float* sw,
-                                   const void* bias, const EpilogueArgs& epi, void* y, int64_t M,
-                                   int64_t N, int64_t K, cudaStream_t stream, bool weights_ready) {
-    if (M < 1 || M > kSmallMaxRows) return NVFP4_ERR_INVALID_ARG;
-    const bool w = weights_ready;
-    if (int8)
-        return launch_small_impl<false, false, true, true>(a, sfa, b, sfb, alpha, bias, y, M, N, K,
-                                                           stream, w, sx, sw, &epi);
-    return sfb_prepared ? launch_small_impl<true, false, false, true>(
-                              a, sfa, b, sfb, alpha, bias, y, M, N, K, stream, w, sx, sw, &epi)
-                        : launch_small_impl<false, false, false, true>(
-                              a, sfa, b, sfb, alpha, bias, y, M, N, K, stream, w, sx, sw, &epi);
+nvfp4_status launch_gemm_small_act(const GemmActArgs& g, cudaStream_t stream) {
+    if (g.M < 1 || g.M > kSmallMaxRows) return NVFP4_ERR_INVALID_ARG;
+    auto run = [&](auto impl) {
+        return impl(g.a, g.sfa, g.b, g.sfb, g.alpha, g.bias, g.y, g.M, g.N, g.K, stream,
+                    g.weights_ready, g.sx, g.sw, &g.epi);
+    };
+    if (g.int8) return run(launch_small_impl<false, false, true, true>);
+    return g.sfb_prepared ? run(launch_small_impl<true, false, false, true>)
+                          : run(launch_small_impl<false, false, false, true>);
 }
 
 }  // namespace nvfp4

@@ -116,22 +116,32 @@ struct EpilogueArgs {
     const void* residual;
 };
 
-nvfp4_status launch_gemm_act(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
-                             const uint8_t* sfb, bool sfb_prepared, const float* alpha,
-                             const void* bias, const EpilogueArgs& epi, void* y, int64_t M,
-                             int64_t N, int64_t K, cudaStream_t stream,
-                             bool weights_ready = false);
-nvfp4_status launch_int8_gemm_act(const int8_t* a, const float* sa, const int8_t* b,
-                                  const float* sb, const void* bias, const EpilogueArgs& epi,
-                                  void* y, int64_t M, int64_t N, int64_t K, cudaStream_t stream);
+// One product with such an epilogue, on NVFP4 (sfa, sfb, alpha) or int8 (sx, sw) operands.
+struct GemmActArgs {
+    bool int8;
+    const uint8_t* a;
+    const uint8_t* b;
+    const uint8_t* sfa;        // NVFP4: 128x4 scales of A
+    const uint8_t* sfb;        // and of B, or its prepared scales
+    bool sfb_prepared;
+    const float* alpha;
+    const float* sx;           // int8: fp32 row scales of A and of B
+    const float* sw;
+    const void* bias;
+    EpilogueArgs epi;
+    void* y;
+    int64_t M, N, K;
+    bool weights_ready;        // as in launch_gemm
+};
 
-// The swapped-operand kernel with the same epilogue, for NVFP4 (sfa, sfb, alpha) or int8
-// (sx, sw) operands; M <= kSmallMaxRows.
-nvfp4_status launch_gemm_small_act(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
-                                   const uint8_t* sfb, bool int8, bool sfb_prepared,
-                                   const float* alpha, const float* sx, const float* sw,
-                                   const void* bias, const EpilogueArgs& epi, void* y, int64_t M,
-                                   int64_t N, int64_t K, cudaStream_t stream, bool weights_ready);
+// Picks the schedule (gemm_pair.cu): the swapped-operand kernel for few rows, split-K for
+// grids of few tiles (taken says whether it was launched), SM pairs for the rest.
+nvfp4_status launch_gemm_act(const GemmActArgs& g, cudaStream_t stream);
+nvfp4_status launch_gemm_small_act(const GemmActArgs& g, cudaStream_t stream);
+nvfp4_status launch_gemm_act_split_k(const GemmActArgs& g, bool* taken, cudaStream_t stream);
+
+// bf16 [M, N] tensor map with a 32 x 32 box and 64-byte swizzle (N % 8 == 0).
+bool make_output_map(CUtensorMap* map, void* base, int64_t M, int64_t N);
 
 // Residual addition, root-mean-square norm and quantization of [rows, K] (norm.cu).
 constexpr int64_t kNormMaxK = 65536;   // 1024 threads x four 16-value units
