@@ -144,37 +144,43 @@ __device__ __forceinline__ void pair_step_fp4_w(uint32_t d, uint64_t ad, uint64_
         : "memory");
 }
 
+// Arrival at a barrier of either CTA.  It hands over tensor memory (ordered by the tcgen05
+// fences around it), no generic writes, so the default scope is enough: a release at cluster
+// scope costs a memory barrier on the path from one tile's accumulator to the next MMA.
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-// The bounded wait of common.cuh for arrivals that come from the other CTA as well.
-__device__ __forceinline__ bool wait_cluster_w(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                               int* status, uint64_t budget_ns) {
-    auto ready = [&]() {
-        uint32_t ok;
+// Bounded wait of a whole warp, converged; lane 0's outcome decides.  Arrivals may come from
+// the other CTA.  The clock and the abort flag are read once in 32 polls: read in every one,
+// the waiting warps kept the pipe that the epilogue's conversions need 92 % busy.
+__device__ __forceinline__ bool pair_wait_w(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                            int* status, uint64_t budget_ns) {
+    const uint32_t addr = smem_u32(bar);
+    bool ok = false;
+    uint64_t t0 = 0;
+    for (uint32_t poll = 1; !ok; ++poll) {
+        uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
+            : "=r"(done)
+            : "r"(addr), "r"(parity)
             : "memory");
-        return ok != 0;
-    };
-    bool ok = ready();
-    if (!ok) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!(ok = ready())) {
-            if (*abort) break;
-            if (globaltimer_ns() - t0 > budget_ns) {
+        ok = __shfl_sync(0xffffffffu, done, 0) != 0;
+        if (!ok && (poll & 31u) == 0u) {
+            if (t0 == 0) t0 = globaltimer_ns();
+            int give_up = *abort;
+            if (!give_up && globaltimer_ns() - t0 > budget_ns) {
                 record_status(status, NVFP4_ERR_TIMEOUT);
                 *abort = 1;
-                break;
+                give_up = 1;
             }
+            if (__shfl_sync(0xffffffffu, give_up, 0)) break;
         }
     }
-    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    return ok;
 }
 
 __device__ __forceinline__ void pair_coords(const PairParams& p, int tile, int& m_blk, int& n_blk) {
@@ -287,7 +293,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             pair_coords(p, tile, m_blk, n_blk);
             for (int kt = 0; kt < p.k_tiles; ++kt, ++fills) {
                 if (fills >= n_early) {
-                    if (!mbar_wait_bounded_warp(&empty[stage], phase ^ 1, abort_flag, p.status,
+                    if (!pair_wait_w(&empty[stage], phase ^ 1, abort_flag, p.status,
                                                 p.budget_ns)) {
                         ok = false;
                         break;
@@ -316,8 +322,8 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             for (int tile = pair; ok && tile < p.tiles; tile += pairs, ++it) {
                 const int b = it & 1;
                 const uint32_t use = (uint32_t)(it >> 1);
-                if (!wait_cluster_w(&acc_free[b], (use & 1) ^ 1, abort_flag, p.status, p.budget_ns) ||
-                    (!I8 && !wait_cluster_w(ovl_free, (uint32_t)(it & 1) ^ 1, abort_flag, p.status,
+                if (!pair_wait_w(&acc_free[b], (use & 1) ^ 1, abort_flag, p.status, p.budget_ns) ||
+                    (!I8 && !pair_wait_w(ovl_free, (uint32_t)(it & 1) ^ 1, abort_flag, p.status,
                                             p.budget_ns))) {
                     ok = false;
                     break;
@@ -325,7 +331,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 tc_fence_after();
                 const uint32_t acc = tmem + (b ? (I8 ? 256u : 192u) : 0u);
                 for (int kt = 0; kt < p.k_tiles; ++kt) {
-                    if (!wait_cluster_w(&full[stage], phase, abort_flag, p.status, p.budget_ns)) {
+                    if (!pair_wait_w(&full[stage], phase, abort_flag, p.status, p.budget_ns)) {
                         ok = false;
                         break;
                     }
@@ -360,7 +366,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             // every tensor-core operation of the pair has finished
             commit_own_w(drain);
             volatile int no_abort = 0;
-            mbar_wait_bounded(drain, 0, &no_abort, p.status, p.budget_ns);
+            pair_wait_w(drain, 0, &no_abort, p.status, p.budget_ns);
         }
         __syncwarp();
     } else {
@@ -424,7 +430,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             if (I8) reinterpret_cast<float2*>(ssw)[lane] = sw2;
             sbias[lane] = bias2;
             __syncwarp();
-            if (!mbar_wait_bounded_warp(&acc_full[b], use & 1, abort_flag, p.status, p.budget_ns)) {
+            if (!pair_wait_w(&acc_full[b], use & 1, abort_flag, p.status, p.budget_ns)) {
                 ok = false;
                 break;
             }
@@ -493,7 +499,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 }
                 uint8_t* sb = stg + s * P_STG;
                 if (res_tma) {
-                    if (!mbar_wait_bounded_warp(&rfull[s], (res_phase >> s) & 1, abort_flag, p.status,
+                    if (!pair_wait_w(&rfull[s], (res_phase >> s) & 1, abort_flag, p.status,
                                                 p.budget_ns))
                         return false;
                     res_phase ^= 1u << s;
@@ -556,7 +562,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         for (int s = 0; s < 2; ++s)
             if (res_ahead & (1u << s)) {
                 volatile int no_abort = 0;
-                mbar_wait_bounded(&rfull[s], (res_phase >> s) & 1, &no_abort, p.status, p.budget_ns);
+                pair_wait_w(&rfull[s], (res_phase >> s) & 1, &no_abort, p.status, p.budget_ns);
             }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
