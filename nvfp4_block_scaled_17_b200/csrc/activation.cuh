@@ -27,6 +27,17 @@ __device__ __forceinline__ float rcp_approx(float v) {
     return r;
 }
 
+// Two fp32 products in one instruction, each rounded by itself.  (The packed sum is not
+// used after it: the two were contracted into one fused multiply-add, written-out rounding
+// or not, and that rounds once where the plain products round twice.)
+__device__ __forceinline__ float2 mul2_rn(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // v / (1 + 2^t).  t is held below 126, so the sum stays finite and its reciprocal normal;
@@ -58,28 +69,40 @@ __device__ __forceinline__ float act_gelu(float v) {
     return fmaf(-z * (t * q), e, fmaxf(v, 0.0f));
 }
 
-// act over the values of v that it applies to: all n, or (gated) the even ones, whose odd
-// neighbour is then multiplied in (the result stays at the even places).
+template <int ACT>
+__device__ __forceinline__ float act_value(float v) {
+    if constexpr (ACT == NVFP4_ACT_RELU) return fmaxf(v, 0.0f);
+    if constexpr (ACT == NVFP4_ACT_GELU) return act_gelu(v);
+    if constexpr (ACT == NVFP4_ACT_GELU_TANH) return act_gelu_tanh(v);
+    if constexpr (ACT == NVFP4_ACT_SILU) return act_silu(v);
+    return v;
+}
+
+// act over the values of v that it applies to: all of them, or (GATED) the even ones, whose
+// odd neighbour is then multiplied in (the result stays at the even places).
+template <int ACT, bool GATED, int N>
+__device__ __forceinline__ void activate(float (&v)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; j += GATED ? 2 : 1) {
+        v[j] = act_value<ACT>(v[j]);
+        if (GATED) v[j] *= v[j + 1];
+    }
+}
+
+// The same with the activation chosen at run time (the reduction phases, few values a thread).
 template <int N>
-__device__ __forceinline__ void apply_activation(float (&v)[N], int act, bool gated) {
-    const int base = act & ~NVFP4_ACT_GATED;
-    auto each = [&](auto f) {
-        if (gated) {
-#pragma unroll
-            for (int j = 0; j < N; j += 2) v[j] = f(v[j]) * v[j + 1];
-        } else {
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[j] = f(v[j]);
-        }
-    };
-    switch (base) {
-        case NVFP4_ACT_RELU: each([](float x) { return fmaxf(x, 0.0f); }); break;
-        case NVFP4_ACT_GELU: each([](float x) { return act_gelu(x); }); break;
-        case NVFP4_ACT_GELU_TANH: each([](float x) { return act_gelu_tanh(x); }); break;
-        case NVFP4_ACT_SILU: each([](float x) { return act_silu(x); }); break;
-        default:
-            if (gated) each([](float x) { return x; });
-            break;
+__device__ __forceinline__ void apply_activation(float (&v)[N], int act) {
+    switch (act) {
+        case NVFP4_ACT_RELU: return activate<NVFP4_ACT_RELU, false>(v);
+        case NVFP4_ACT_GELU: return activate<NVFP4_ACT_GELU, false>(v);
+        case NVFP4_ACT_GELU_TANH: return activate<NVFP4_ACT_GELU_TANH, false>(v);
+        case NVFP4_ACT_SILU: return activate<NVFP4_ACT_SILU, false>(v);
+        case NVFP4_ACT_GATED: return activate<NVFP4_ACT_NONE, true>(v);
+        case NVFP4_ACT_GATED + NVFP4_ACT_RELU: return activate<NVFP4_ACT_RELU, true>(v);
+        case NVFP4_ACT_GATED + NVFP4_ACT_GELU: return activate<NVFP4_ACT_GELU, true>(v);
+        case NVFP4_ACT_GATED + NVFP4_ACT_GELU_TANH: return activate<NVFP4_ACT_GELU_TANH, true>(v);
+        case NVFP4_ACT_GATED + NVFP4_ACT_SILU: return activate<NVFP4_ACT_SILU, true>(v);
+        default: return;
     }
 }
 
@@ -129,7 +152,7 @@ __device__ __forceinline__ void reduce_granule(float (&v)[4], uint32_t off, int 
 __device__ __forceinline__ void finish_granule(float (&v)[4], int act, bool gated,
                                                const uint16_t* residual, uint16_t* y, int64_t row,
                                                int n, int n_out) {
-    apply_activation(v, act, gated);
+    apply_activation(v, act);
     if (gated) {
         const int col = n >> 1;
         const int64_t at = row * n_out + col;

@@ -47,7 +47,8 @@ constexpr int PS_OP = PROWS * PKB;            // 16 KiB: A, and B
 constexpr int PS_SFA = 4 * 512;
 constexpr int PS_SFB = 8 * 512;
 constexpr int P_STG = 32 * 64;                // one 32 x 32 bf16 staging tile; two per warp
-constexpr int P_COLS = 64 * 4 + 64 * 2;       // a warp's column scales (int8) and bias
+constexpr int P_COLS = 64 * 4 + 64 * 4;       // a warp's column scales (int8) and bias, fp32
+constexpr int P_GROUP = 8;                    // row blocks of a supertile
 template <bool I8>
 struct PairSmem {
     static constexpr int STAGE = 2 * PS_OP + (I8 ? 0 : PS_SFA + PS_SFB);
@@ -70,12 +71,10 @@ struct PairParams {
     const uint16_t* residual;  // bf16 [M, n_out] or null
     uint16_t* y;               // bf16 [M, n_out]
     int M, N, n_out;
-    int act, gated;
     int m_blocks, n_blocks, tiles;
     int k_tiles;               // stages of K
     int kchunks;               // 32-byte K steps
     int prepared;              // B scales: 1 = prepared blocks, 0 = 128x4 chunks
-    int n_fast;
     int tma_store;             // n_out % 8 == 0
     int w_early;               // B was complete before the previous kernel started
     int* status;
@@ -183,17 +182,18 @@ __device__ __forceinline__ bool pair_wait_w(uint64_t* bar, uint32_t parity, vola
     return ok;
 }
 
+// Tile order: supertiles of eight row blocks, walked column block by column block, so the
+// 74 tiles in flight share about as many panels of A as of B (8192^3 int8: 685 MB of DRAM
+// reads when they walked whole rows of tiles, the operands being 134 MB).
 __device__ __forceinline__ void pair_coords(const PairParams& p, int tile, int& m_blk, int& n_blk) {
-    if (p.n_fast) {
-        m_blk = tile / p.n_blocks;
-        n_blk = tile - m_blk * p.n_blocks;
-    } else {
-        n_blk = tile / p.m_blocks;
-        m_blk = tile - n_blk * p.m_blocks;
-    }
+    const int super = tile / (P_GROUP * p.n_blocks);
+    const int rest = tile - super * P_GROUP * p.n_blocks;
+    const int rows = min(P_GROUP, p.m_blocks - super * P_GROUP);
+    n_blk = rest / rows;
+    m_blk = super * P_GROUP + rest - n_blk * rows;
 }
 
-template <bool I8>
+template <bool I8, int ACT, bool GATED>
 __global__ void __launch_bounds__(PTHREADS, 1)
 gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
@@ -374,13 +374,12 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const int quad = warp & 3;               // tensor-memory lanes 32 quad .. + 31
         const int quarter = e >> 2;              // columns 64 quarter .. + 63
         uint8_t* stg = sStg + e * 2 * P_STG;
-        float* ssw = reinterpret_cast<float*>(sCols + e * P_COLS);
-        uint32_t* sbias = reinterpret_cast<uint32_t*>(sCols + e * P_COLS + 256);
+        float* ssw = reinterpret_cast<float*>(sCols + e * P_COLS);   // 64 column scales (int8)
+        float* sbias = ssw + 64;                                     // 64 bias values
         uint64_t* rfull = res_full + 2 * e;
         const uint32_t free0 = dsmem_addr(smem_u32(acc_free), 0);
         const uint32_t ovl0 = dsmem_addr(smem_u32(ovl_free), 0);
         const float alpha = I8 ? 0.0f : *p.alpha;
-        const bool gated = p.gated != 0;
         const bool res_tma = p.residual && p.tma_store;
         uint32_t res_phase = 0, res_ahead = 0;   // per staging tile: parity; loaded, not used
         // Loads the residual chunks of `tile` into the staging tiles that its output will take:
@@ -392,9 +391,9 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const int row = m_blk * 2 * PROWS + rank * PROWS + quad * 32;
             const int n0 = n_blk * PN + quarter * 64;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int col = gated ? n0 >> 1 : n0 + 32 * c;
-                if ((gated && c) || col >= p.n_out) continue;
+            for (int c = 0; c < (GATED ? 1 : 2); ++c) {
+                const int col = GATED ? n0 >> 1 : n0 + 32 * c;
+                if (col >= p.n_out) continue;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&rfull[c], P_STG);
                     tma_load_2d(stg + c * P_STG, &tmR, &rfull[c], col, row);
@@ -402,7 +401,30 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 res_ahead |= 1u << c;
             }
         };
+        // This lane's two columns of a tile (scale, bias) and its row's scale, fetched a tile
+        // ahead.  Columns past N repeat the last one; they are not stored.
+        float2 sw2 = make_float2(0.0f, 0.0f), bias2 = make_float2(0.0f, 0.0f);
+        float row_scale = alpha;
+        auto fetch_columns = [&](int tile) {
+            if (tile >= p.tiles) return;
+            int m_blk, n_blk;
+            pair_coords(p, tile, m_blk, n_blk);
+            const int n = n_blk * PN + quarter * 64 + 2 * lane;
+            if (p.bias) {
+                const uint32_t w = n + 2 <= p.N ? *reinterpret_cast<const uint32_t*>(p.bias + n)
+                                                : (uint32_t)p.bias[min(n, p.N - 1)] |
+                                                      ((uint32_t)p.bias[min(n + 1, p.N - 1)] << 16);
+                bias2 = make_float2(bf16lo(w), bf16hi(w));
+            }
+            if constexpr (I8) {
+                sw2 = n + 2 <= p.N ? *reinterpret_cast<const float2*>(p.sw + n)
+                                   : make_float2(p.sw[min(n, p.N - 1)], p.sw[min(n + 1, p.N - 1)]);
+                const int row = m_blk * 2 * PROWS + rank * PROWS + quad * 32 + lane;
+                row_scale = row < p.M ? p.sx[row] : 0.0f;
+            }
+        };
         if (res_tma) load_residual(pair);
+        fetch_columns(pair);
         int it = 0;
         bool ok = true;
         for (int tile = pair; ok && tile < p.tiles; tile += pairs, ++it) {
@@ -412,34 +434,21 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const uint32_t use = (uint32_t)(it >> 1);
             const int row0 = m_blk * 2 * PROWS + rank * PROWS + quad * 32;
             const int n0 = n_blk * PN + quarter * 64;
-            // this warp's column values, before the accumulator wait (columns past N repeat
-            // the last one; they are not stored)
-            const int n = n0 + 2 * lane;
-            float2 sw2 = make_float2(0.0f, 0.0f);
-            uint32_t bias2 = 0u;
-            if (I8) {
-                if (n + 2 <= p.N) sw2 = *reinterpret_cast<const float2*>(p.sw + n);
-                else sw2 = make_float2(p.sw[min(n, p.N - 1)], p.sw[min(n + 1, p.N - 1)]);
-            }
-            if (p.bias) {
-                if (n + 2 <= p.N) bias2 = *reinterpret_cast<const uint32_t*>(p.bias + n);
-                else bias2 = (uint32_t)p.bias[min(n, p.N - 1)] | ((uint32_t)p.bias[min(n + 1, p.N - 1)] << 16);
-            }
-            const float scale = I8 ? (row0 + lane < p.M ? p.sx[row0 + lane] : 0.0f) : alpha;
             __syncwarp();                        // the last tile's values have been read
             if (I8) reinterpret_cast<float2*>(ssw)[lane] = sw2;
-            sbias[lane] = bias2;
+            reinterpret_cast<float2*>(sbias)[lane] = bias2;
+            const float scale = row_scale;
             __syncwarp();
             if (!pair_wait_w(&acc_full[b], use & 1, abort_flag, p.status, p.budget_ns)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            uint32_t r0[32], r1[32];
+            uint32_t r[2][32];
             const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + (b ? (I8 ? 256u : 192u) : 0u) +
                                 (uint32_t)(quarter * 64);
-            tmem_ld32(at, r0);
-            tmem_ld32(at + 32, r1);
+            tmem_ld32(at, r[0]);
+            tmem_ld32(at + 32, r[1]);
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
@@ -448,113 +457,127 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 if (!I8 && quarter == (b ? 0 : 3)) arrive_cluster(ovl0);
                 arrive_cluster(free0 + 8u * (uint32_t)b);
             }
+            fetch_columns(tile + pairs);
 
-            auto values = [&](uint32_t (&r)[32], int c) {
-                float v[32];
+            // Eight columns 8 g .. 8 g + 7 of chunk c: scale, bias, activation.
+            auto columns8 = [&](int c, int g, float (&v)[8]) {
+                const float4* b4 = reinterpret_cast<const float4*>(sbias) + 8 * c + 2 * g;
+                const float4* s4 = reinterpret_cast<const float4*>(ssw) + 8 * c + 2 * g;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = 0; q < 2; ++q) {
+                    const float4 bb = b4[q];
+                    float2 lo, hi;
                     if constexpr (I8) {
-                        const float4 s4 = reinterpret_cast<const float4*>(ssw)[8 * c + q];
-                        v[4 * q] = __fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * q]), scale), s4.x);
-                        v[4 * q + 1] = __fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * q + 1]), scale), s4.y);
-                        v[4 * q + 2] = __fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * q + 2]), scale), s4.z);
-                        v[4 * q + 3] = __fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * q + 3]), scale), s4.w);
+                        const float4 ss = s4[q];
+                        lo = make_float2(__int2float_rn((int)r[c][8 * g + 4 * q]),
+                                         __int2float_rn((int)r[c][8 * g + 4 * q + 1]));
+                        hi = make_float2(__int2float_rn((int)r[c][8 * g + 4 * q + 2]),
+                                         __int2float_rn((int)r[c][8 * g + 4 * q + 3]));
+                        lo = mul2_rn(mul2_rn(lo, make_float2(scale, scale)), make_float2(ss.x, ss.y));
+                        hi = mul2_rn(mul2_rn(hi, make_float2(scale, scale)), make_float2(ss.z, ss.w));
                     } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) v[4 * q + j] = __fmul_rn(scale, __uint_as_float(r[4 * q + j]));
+                        lo = make_float2(__uint_as_float(r[c][8 * g + 4 * q]),
+                                         __uint_as_float(r[c][8 * g + 4 * q + 1]));
+                        hi = make_float2(__uint_as_float(r[c][8 * g + 4 * q + 2]),
+                                         __uint_as_float(r[c][8 * g + 4 * q + 3]));
+                        lo = mul2_rn(lo, make_float2(scale, scale));
+                        hi = mul2_rn(hi, make_float2(scale, scale));
                     }
+                    v[4 * q] = __fadd_rn(lo.x, bb.x);
+                    v[4 * q + 1] = __fadd_rn(lo.y, bb.y);
+                    v[4 * q + 2] = __fadd_rn(hi.x, bb.z);
+                    v[4 * q + 3] = __fadd_rn(hi.y, bb.w);
                 }
-                if (p.bias) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint4 w = reinterpret_cast<const uint4*>(sbias)[4 * c + q];
-                        const uint32_t bw[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            v[8 * q + 2 * j] = __fadd_rn(v[8 * q + 2 * j], bf16lo(bw[j]));
-                            v[8 * q + 2 * j + 1] = __fadd_rn(v[8 * q + 2 * j + 1], bf16hi(bw[j]));
-                        }
-                    }
-                }
-                apply_activation(v, p.act, gated);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(v[j]);
+                activate<ACT, GATED>(v);
             };
-            // One output chunk u(0) .. u(31) at column col: residual, rounding, store.
-            auto store = [&](auto u, int s, int col) -> bool {
-                if (!p.tma_store) {
-                    const int row = row0 + lane;
-                    if (row < p.M) {
-                        const size_t o = (size_t)row * p.n_out + col;
+            // Output values 8 o .. 8 o + 7 of chunk c: one 8-column group, or, gated, the even
+            // places of two.
+            auto outputs8 = [&](int c, int o, float (&u)[8]) {
+                if constexpr (GATED) {
+                    float v[8];
+                    columns8(o >> 1, 2 * (o & 1), v);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < 4; ++j) u[j] = v[2 * j];
+                    columns8(o >> 1, 2 * (o & 1) + 1, v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) u[4 + j] = v[2 * j];
+                } else {
+                    columns8(c, o, u);
+                }
+            };
+            if (p.tma_store) {
+                bool stored = false;
+#pragma unroll
+                for (int c = 0; c < (GATED ? 1 : 2); ++c) {
+                    const int col = GATED ? n0 >> 1 : n0 + 32 * c;
+                    if (!ok || col >= p.n_out) continue;     // warp-uniform
+                    uint8_t* sb = stg + c * P_STG;
+                    if (res_tma) {
+                        ok = pair_wait_w(&rfull[c], (res_phase >> c) & 1, abort_flag, p.status, p.budget_ns);
+                        if (!ok) continue;
+                        res_phase ^= 1u << c;
+                        res_ahead &= ~(1u << c);
+                    }
+                    // 64-byte swizzle: 16-byte piece o of row r sits at o ^ ((r >> 1) & 3)
+#pragma unroll
+                    for (int o = 0; o < 4; ++o) {
+                        float u[8];
+                        outputs8(c, o, u);
+                        uint4* to = reinterpret_cast<uint4*>(sb + lane * 64 + ((o ^ ((lane >> 1) & 3)) << 4));
+                        uint32_t w[4];
+                        if (res_tma) {
+                            const uint4 t = *to;
+                            const uint32_t rw[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                u[2 * j] = __fadd_rn(u[2 * j], bf16lo(rw[j]));
+                                u[2 * j + 1] = __fadd_rn(u[2 * j + 1], bf16hi(rw[j]));
+                            }
+                        } else if (c == 0 && o == 0) {
+                            // the last tile's stores have read the staging tiles
+                            if (lane == 0) bulk_wait_read<0>();
+                            __syncwarp();
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[j] = bf16x2_rn(u[2 * j], u[2 * j + 1]);
+                        *to = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    stored = true;
+                }
+                if (stored) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&tmY, stg, GATED ? n0 >> 1 : n0, row0);
+                        if (!GATED && n0 + 32 < p.n_out) tma_store_2d(&tmY, stg + P_STG, n0 + 32, row0);
+                        bulk_commit();
+                    }
+                }
+                if (ok && res_tma) {
+                    if (lane == 0) bulk_wait_read<0>();
+                    __syncwarp();
+                    load_residual(tile + pairs);
+                }
+            } else {
+                // rows of y are not 16-byte multiples: element by element
+                const int row = row0 + lane;
+#pragma unroll
+                for (int c = 0; c < (GATED ? 1 : 2); ++c)
+#pragma unroll
+                    for (int o = 0; o < 4; ++o) {
+                        float u[8];
+                        outputs8(c, o, u);
+                        const int col = (GATED ? n0 >> 1 : n0 + 32 * c) + 8 * o;
+                        if (row >= p.M) continue;
+                        const size_t to = (size_t)row * p.n_out + col;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
                             if (col + j < p.n_out) {
-                                float t = u(j);
                                 if (p.residual)
-                                    t = __fadd_rn(t, __uint_as_float((uint32_t)p.residual[o + j] << 16));
-                                p.y[o + j] = (uint16_t)bf16x2_rn(t, 0.0f);
+                                    u[j] = __fadd_rn(u[j], __uint_as_float((uint32_t)p.residual[to + j] << 16));
+                                p.y[to + j] = (uint16_t)bf16x2_rn(u[j], 0.0f);
                             }
                     }
-                    return true;
-                }
-                uint8_t* sb = stg + s * P_STG;
-                if (res_tma) {
-                    if (!pair_wait_w(&rfull[s], (res_phase >> s) & 1, abort_flag, p.status,
-                                                p.budget_ns))
-                        return false;
-                    res_phase ^= 1u << s;
-                    res_ahead &= ~(1u << s);
-                }
-                // 64-byte swizzle: 16-byte chunk c of row r sits at c ^ ((r >> 1) & 3)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint4* o = reinterpret_cast<uint4*>(sb + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
-                    uint32_t w[4];
-                    if (res_tma) {
-                        const uint4 t = *o;
-                        const uint32_t rw[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            w[j] = bf16x2_rn(__fadd_rn(u(8 * c + 2 * j), bf16lo(rw[j])),
-                                             __fadd_rn(u(8 * c + 2 * j + 1), bf16hi(rw[j])));
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) w[j] = bf16x2_rn(u(8 * c + 2 * j), u(8 * c + 2 * j + 1));
-                    }
-                    *o = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    tma_store_2d(&tmY, sb, col, row0);
-                    bulk_commit();
-                }
-                return true;
-            };
-            // A staging tile is free when the last tile's stores have read it; with a
-            // residual that was waited for before the residual was loaded.
-            if (!res_tma && p.tma_store) {
-                if (lane == 0) bulk_wait_read<0>();
-                __syncwarp();
-            }
-            if (n0 < p.N) values(r0, 0);         // warp-uniform, here and below
-            if (n0 >= p.N) {
-            } else if (gated) {
-                if (n0 + 32 < p.N) values(r1, 1);
-                ok = store([&](int j) {
-                    return __uint_as_float(j < 16 ? r0[2 * (j & 15)] : r1[2 * (j & 15)]);
-                }, 0, n0 >> 1);
-            } else {
-                ok = store([&](int j) { return __uint_as_float(r0[j]); }, 0, n0);
-                if (ok && n0 + 32 < p.N) {
-                    values(r1, 1);
-                    ok = store([&](int j) { return __uint_as_float(r1[j]); }, 1, n0 + 32);
-                }
-            }
-            if (ok && res_tma) {
-                if (lane == 0) bulk_wait_read<0>();
-                __syncwarp();
-                load_residual(tile + pairs);
             }
         }
         // residual chunks still on their way must land before the block can exit
@@ -592,6 +615,21 @@ bool make_scale_map(CUtensorMap* map, const void* base, int64_t chunks) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+using PairKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
+                            CUtensorMap, PairParams);
+
+template <bool I8>
+PairKernel pair_kernel(int activation) {
+    static const PairKernel table[2][5] = {
+        {gemm_pair_kernel<I8, NVFP4_ACT_NONE, false>, gemm_pair_kernel<I8, NVFP4_ACT_RELU, false>,
+         gemm_pair_kernel<I8, NVFP4_ACT_GELU, false>, gemm_pair_kernel<I8, NVFP4_ACT_GELU_TANH, false>,
+         gemm_pair_kernel<I8, NVFP4_ACT_SILU, false>},
+        {gemm_pair_kernel<I8, NVFP4_ACT_NONE, true>, gemm_pair_kernel<I8, NVFP4_ACT_RELU, true>,
+         gemm_pair_kernel<I8, NVFP4_ACT_GELU, true>, gemm_pair_kernel<I8, NVFP4_ACT_GELU_TANH, true>,
+         gemm_pair_kernel<I8, NVFP4_ACT_SILU, true>}};
+    return table[(activation & NVFP4_ACT_GATED) ? 1 : 0][activation & ~NVFP4_ACT_GATED];
+}
+
 template <bool I8>
 nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
     DeviceInfo dev;
@@ -599,12 +637,14 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
     if (st != NVFP4_OK) return st;
     int* status = nullptr;
     if ((st = status_word(&status)) != NVFP4_OK) return st;
-    static std::atomic<int> attr_set[64];
-    if (!attr_set[dev.device & 63].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(gemm_pair_kernel<I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const PairKernel kernel = pair_kernel<I8>(g.epi.activation);
+    static std::atomic<int> attr_set[64][32];
+    std::atomic<int>& set = attr_set[dev.device & 63][g.epi.activation & 31];
+    if (!set.load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  PairSmem<I8>::BYTES) != cudaSuccess)
             return NVFP4_ERR_CUDA;
-        attr_set[dev.device & 63].store(1, std::memory_order_release);
+        set.store(1, std::memory_order_release);
     }
     PairParams p{};
     const int64_t kbytes = I8 ? g.K : g.K / 2;
@@ -616,16 +656,13 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
     p.y = static_cast<uint16_t*>(g.y);
     p.M = (int)g.M;
     p.N = (int)g.N;
-    p.act = g.epi.activation;
-    p.gated = (g.epi.activation & NVFP4_ACT_GATED) ? 1 : 0;
-    p.n_out = (int)(p.gated ? g.N / 2 : g.N);
+    p.n_out = (int)((g.epi.activation & NVFP4_ACT_GATED) ? g.N / 2 : g.N);
     p.m_blocks = (int)((g.M + 2 * PROWS - 1) / (2 * PROWS));
     p.n_blocks = (int)((g.N + PN - 1) / PN);
     p.tiles = p.m_blocks * p.n_blocks;
     p.k_tiles = (int)((kbytes + PKB - 1) / PKB);
     p.kchunks = (int)(kbytes / 32);
     p.prepared = g.sfb_prepared ? 1 : 0;
-    p.n_fast = g.N <= g.M ? 1 : 0;
     p.tma_store = p.n_out % 8 == 0;
     p.w_early = g.weights_ready ? 1 : 0;
     p.status = status;
@@ -663,7 +700,7 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<I8>, mapA, mapB, mapSFA, mapSFB, mapY, mapR, p) ==
+    return cudaLaunchKernelEx(&cfg, kernel, mapA, mapB, mapSFA, mapSFB, mapY, mapR, p) ==
                    cudaSuccess
                ? NVFP4_OK
                : NVFP4_ERR_CUDA;
