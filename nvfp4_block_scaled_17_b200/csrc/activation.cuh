@@ -1,4 +1,4 @@
-// activation.cuh -- the activations of the GEMM epilogues, in fp32.
+// activation.cuh -- the activations of the GEMM epilogues, in fp32, two values at a time.
 //
 //   relu       max(v, 0)
 //   gelu       v * Phi(v), Phi the normal distribution function
@@ -6,9 +6,13 @@
 //   silu       v / (1 + exp(-v))
 // A gated epilogue takes column pairs: u[j] = act(v[2j]) * v[2j + 1].
 //
-// Two special-function operations per value (one exponential, one reciprocal), the rest on
-// the FMA pipe.  Errors against 64-bit values, before the one rounding to bf16 (2^-9
-// relative): below 5e-7 max(|v|, 1).
+// The last three are all v * s(L(v)), s the logistic function: L = v for silu, an odd cubic
+// for gelu_tanh ((1 + tanh z) / 2 = s(2 z)), and for gelu the logit of Phi, an odd function
+// that a polynomial of degree 13 meets to 7e-8 in v * Phi(v).  One exponential per value and
+// one reciprocal per two (1 / a and 1 / b from 1 / (a b)) keep the special-function pipe,
+// which takes 8 cycles per warp and operation, below the FMA pipe; the rest is packed
+// fp32x2 arithmetic.  Errors against 64-bit values, before the one rounding to bf16:
+// below 5e-7 max(|v|, 1).
 #pragma once
 
 #include "common.cuh"
@@ -40,52 +44,52 @@ __device__ __forceinline__ float2 mul2_rn(float2 a, float2 b) {
 }
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// v / (1 + 2^t).  t is held below 126, so the sum stays finite and its reciprocal normal;
-// there the quotient is v 2^-126, zero to every bf16 that it can be added to.
-__device__ __forceinline__ float over_one_plus_exp2(float v, float t) {
-    return v * rcp_approx(1.0f + ex2_approx(fminf(t, 126.0f)));
-}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-__device__ __forceinline__ float act_silu(float v) { return over_one_plus_exp2(v, -kLog2e * v); }
-
-// (1 + tanh(z)) / 2 = 1 / (1 + exp(-2 z))
-__device__ __forceinline__ float act_gelu_tanh(float v) {
-    constexpr float c = -2.0f * 0.79788456080286535588f * kLog2e;
-    return over_one_plus_exp2(v, v * fmaf(c * 0.044715f, v * v, c));
-}
-
-// v Phi(v) = max(v, 0) - |v| Q(|v|), Q(z) = erfc(z / sqrt 2) / 2 by the rational form of
-// Hastings ("Approximations for Digital Computers", sheet 45; also Abramowitz and Stegun
-// 7.1.26, |error of erf| <= 1.5e-7): erfc(y) = t (a1 + t (a2 + ...)) exp(-y^2),
-// t = 1 / (1 + p y).
-__device__ __forceinline__ float act_gelu(float v) {
-    const float z = fabsf(v);
-    const float t = rcp_approx(fmaf(0.3275911f * 0.70710678118654752440f, z, 1.0f));
-    float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
-    q = fmaf(t, q, 0.5f * 1.421413741f);
-    q = fmaf(t, q, 0.5f * -0.284496736f);
-    q = fmaf(t, q, 0.5f * 0.254829592f);
-    const float e = ex2_approx((-0.5f * kLog2e) * z * z);
-    return fmaf(-z * (t * q), e, fmaxf(v, 0.0f));
+// -log2(e) L(v) of the two values.
+template <int ACT>
+__device__ __forceinline__ float2 minus_logit2(float2 v) {
+    if constexpr (ACT == NVFP4_ACT_SILU) return __fmul2_rn(v, both(-kLog2e));
+    float2 u = __fmul2_rn(v, v);
+    if constexpr (ACT == NVFP4_ACT_GELU_TANH) {
+        constexpr float c = -2.0f * 0.79788456080286535588f * kLog2e;
+        return __fmul2_rn(v, __ffma2_rn(u, both(c * 0.044715f), both(c)));
+    }
+    // gelu: logit Phi(v) = v Q(v^2); Q fitted on |v| <= 6 for the least largest error of
+    // v Phi(v), and held at its value there beyond
+    u = make_float2(fminf(u.x, 36.0f), fminf(u.y, 36.0f));
+    float2 q = __ffma2_rn(u, both(-kLog2e * 3.6392367769551445e-09f), both(-kLog2e * -2.680700010037935e-07f));
+    q = __ffma2_rn(u, q, both(-kLog2e * 7.956275638921296e-06f));
+    q = __ffma2_rn(u, q, both(-kLog2e * -0.00011060688607769335f));
+    q = __ffma2_rn(u, q, both(-kLog2e * -6.584639140541981e-05f));
+    q = __ffma2_rn(u, q, both(-kLog2e * 0.07266800159418906f));
+    q = __ffma2_rn(u, q, both(-kLog2e * 1.5957686572495096f));
+    return __fmul2_rn(v, q);
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_value(float v) {
-    if constexpr (ACT == NVFP4_ACT_RELU) return fmaxf(v, 0.0f);
-    if constexpr (ACT == NVFP4_ACT_GELU) return act_gelu(v);
-    if constexpr (ACT == NVFP4_ACT_GELU_TANH) return act_gelu_tanh(v);
-    if constexpr (ACT == NVFP4_ACT_SILU) return act_silu(v);
-    return v;
+__device__ __forceinline__ float2 act_value2(float2 v) {
+    if constexpr (ACT == NVFP4_ACT_NONE) return v;
+    if constexpr (ACT == NVFP4_ACT_RELU) return make_float2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f));
+    const float2 t = minus_logit2<ACT>(v);
+    // exponents below 60 keep the product of two sums below 2^122; at 60 the quotient is
+    // v 2^-60, far below every bf16 next to which it could count
+    const float2 d = __fadd2_rn(
+        make_float2(ex2_approx(fminf(t.x, 60.0f)), ex2_approx(fminf(t.y, 60.0f))), both(1.0f));
+    const float r = rcp_approx(d.x * d.y);
+    return __fmul2_rn(v, __fmul2_rn(both(r), make_float2(d.y, d.x)));
 }
 
 // act over the values of v that it applies to: all of them, or (GATED) the even ones, whose
 // odd neighbour is then multiplied in (the result stays at the even places).
 template <int ACT, bool GATED, int N>
 __device__ __forceinline__ void activate(float (&v)[N]) {
+    constexpr int D = GATED ? 2 : 1;
 #pragma unroll
-    for (int j = 0; j < N; j += GATED ? 2 : 1) {
-        v[j] = act_value<ACT>(v[j]);
-        if (GATED) v[j] *= v[j + 1];
+    for (int j = 0; j < N; j += 2 * D) {
+        const float2 u = act_value2<ACT>(make_float2(v[j], v[j + D]));
+        v[j] = GATED ? u.x * v[j + 1] : u.x;
+        v[j + D] = GATED ? u.y * v[j + 3] : u.y;
     }
 }
 

@@ -72,6 +72,7 @@ struct PairParams {
     uint16_t* y;               // bf16 [M, n_out]
     int M, N, n_out;
     int m_blocks, n_blocks, tiles;
+    FastDiv div_super, div_last;   // by the tiles of a supertile, by the last one's rows
     int k_tiles;               // stages of K
     int kchunks;               // 32-byte K steps
     int prepared;              // B scales: 1 = prepared blocks, 0 = 128x4 chunks
@@ -186,11 +187,11 @@ __device__ __forceinline__ bool pair_wait_w(uint64_t* bar, uint32_t parity, vola
 // 74 tiles in flight share about as many panels of A as of B (8192^3 int8: 685 MB of DRAM
 // reads when they walked whole rows of tiles, the operands being 134 MB).
 __device__ __forceinline__ void pair_coords(const PairParams& p, int tile, int& m_blk, int& n_blk) {
-    const int super = tile / (P_GROUP * p.n_blocks);
+    const int super = (int)fast_div((uint32_t)tile, p.div_super);
     const int rest = tile - super * P_GROUP * p.n_blocks;
-    const int rows = min(P_GROUP, p.m_blocks - super * P_GROUP);
-    n_blk = rest / rows;
-    m_blk = super * P_GROUP + rest - n_blk * rows;
+    const int rows = p.m_blocks - super * P_GROUP;
+    n_blk = rows >= P_GROUP ? rest / P_GROUP : (int)fast_div((uint32_t)rest, p.div_last);
+    m_blk = super * P_GROUP + rest - n_blk * min(rows, P_GROUP);
 }
 
 template <bool I8, int ACT, bool GATED>
@@ -382,14 +383,10 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const float alpha = I8 ? 0.0f : *p.alpha;
         const bool res_tma = p.residual && p.tma_store;
         uint32_t res_phase = 0, res_ahead = 0;   // per staging tile: parity; loaded, not used
-        // Loads the residual chunks of `tile` into the staging tiles that its output will take:
-        // chunk c in staging tile c (one chunk when gated).
-        auto load_residual = [&](int tile) {
-            if (tile >= p.tiles) return;
-            int m_blk, n_blk;
-            pair_coords(p, tile, m_blk, n_blk);
-            const int row = m_blk * 2 * PROWS + rank * PROWS + quad * 32;
-            const int n0 = n_blk * PN + quarter * 64;
+        // Loads the residual chunks of the warp's part of a tile (rows from row, columns from
+        // n0) into the staging tiles that its output will take: chunk c in staging tile c (one
+        // chunk when gated).
+        auto load_residual = [&](int row, int n0) {
 #pragma unroll
             for (int c = 0; c < (GATED ? 1 : 2); ++c) {
                 const int col = GATED ? n0 >> 1 : n0 + 32 * c;
@@ -405,11 +402,8 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         // ahead.  Columns past N repeat the last one; they are not stored.
         float2 sw2 = make_float2(0.0f, 0.0f), bias2 = make_float2(0.0f, 0.0f);
         float row_scale = alpha;
-        auto fetch_columns = [&](int tile) {
-            if (tile >= p.tiles) return;
-            int m_blk, n_blk;
-            pair_coords(p, tile, m_blk, n_blk);
-            const int n = n_blk * PN + quarter * 64 + 2 * lane;
+        auto fetch_columns = [&](int row, int n0) {
+            const int n = n0 + 2 * lane;
             if (p.bias) {
                 const uint32_t w = n + 2 <= p.N ? *reinterpret_cast<const uint32_t*>(p.bias + n)
                                                 : (uint32_t)p.bias[min(n, p.N - 1)] |
@@ -419,21 +413,28 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             if constexpr (I8) {
                 sw2 = n + 2 <= p.N ? *reinterpret_cast<const float2*>(p.sw + n)
                                    : make_float2(p.sw[min(n, p.N - 1)], p.sw[min(n + 1, p.N - 1)]);
-                const int row = m_blk * 2 * PROWS + rank * PROWS + quad * 32 + lane;
-                row_scale = row < p.M ? p.sx[row] : 0.0f;
+                row_scale = row + lane < p.M ? p.sx[row + lane] : 0.0f;
             }
         };
-        if (res_tma) load_residual(pair);
-        fetch_columns(pair);
+        int next_row = 0, next_n0 = 0;           // the warp's part of the next tile
+        auto next_part = [&](int tile) {
+            int m_blk, n_blk;
+            pair_coords(p, tile, m_blk, n_blk);
+            next_row = m_blk * 2 * PROWS + rank * PROWS + quad * 32;
+            next_n0 = n_blk * PN + quarter * 64;
+        };
+        if (pair < p.tiles) {
+            next_part(pair);
+            if (res_tma) load_residual(next_row, next_n0);
+            fetch_columns(next_row, next_n0);
+        }
         int it = 0;
         bool ok = true;
         for (int tile = pair; ok && tile < p.tiles; tile += pairs, ++it) {
-            int m_blk, n_blk;
-            pair_coords(p, tile, m_blk, n_blk);
             const int b = it & 1;
             const uint32_t use = (uint32_t)(it >> 1);
-            const int row0 = m_blk * 2 * PROWS + rank * PROWS + quad * 32;
-            const int n0 = n_blk * PN + quarter * 64;
+            const int row0 = next_row, n0 = next_n0;
+            const bool more = tile + pairs < p.tiles;
             __syncwarp();                        // the last tile's values have been read
             if (I8) reinterpret_cast<float2*>(ssw)[lane] = sw2;
             reinterpret_cast<float2*>(sbias)[lane] = bias2;
@@ -457,7 +458,10 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 if (!I8 && quarter == (b ? 0 : 3)) arrive_cluster(ovl0);
                 arrive_cluster(free0 + 8u * (uint32_t)b);
             }
-            fetch_columns(tile + pairs);
+            if (more) {
+                next_part(tile + pairs);
+                fetch_columns(next_row, next_n0);
+            }
 
             // Eight columns 8 g .. 8 g + 7 of chunk c: scale, bias, activation.
             auto columns8 = [&](int c, int g, float (&v)[8]) {
@@ -553,10 +557,10 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         bulk_commit();
                     }
                 }
-                if (ok && res_tma) {
+                if (ok && more && res_tma) {
                     if (lane == 0) bulk_wait_read<0>();
                     __syncwarp();
-                    load_residual(tile + pairs);
+                    load_residual(next_row, next_n0);
                 }
             } else {
                 // rows of y are not 16-byte multiples: element by element
@@ -660,6 +664,8 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
     p.m_blocks = (int)((g.M + 2 * PROWS - 1) / (2 * PROWS));
     p.n_blocks = (int)((g.N + PN - 1) / PN);
     p.tiles = p.m_blocks * p.n_blocks;
+    p.div_super = make_fastdiv((uint32_t)(P_GROUP * p.n_blocks));
+    p.div_last = make_fastdiv((uint32_t)(p.m_blocks % P_GROUP ? p.m_blocks % P_GROUP : P_GROUP));
     p.k_tiles = (int)((kbytes + PKB - 1) / PKB);
     p.kchunks = (int)(kbytes / 32);
     p.prepared = g.sfb_prepared ? 1 : 0;
