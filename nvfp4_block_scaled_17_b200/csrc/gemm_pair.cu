@@ -16,12 +16,13 @@
 //               Every load signals the leader's full barrier (cta_group::2 loads may).
 //   warp 1      in the leader: MMA issue for both SMs (M = 256, N = 256), the whole warp
 //               converged, one election per K step; commits arrive at both CTAs' barriers.
-//   warps 2-17  epilogue of the CTA's 128 rows: four warps per tensor-memory quadrant, each
-//               64 columns wide, which it reads into 64 registers at once.  So the
-//               accumulator is released as soon as it has been read, before any of it is
-//               scaled, activated or stored, and the next tile's MMAs overlap all of that.
-//               Output chunks of 32 x 32 go through a swizzled staging tile and a TMA store;
-//               with a residual, its chunk is loaded into the same staging tile a tile ahead.
+//   warps 2-17  epilogue of the CTA's 128 rows, two groups of eight warps that take the
+//               tiles in turn, so the latencies of one (tensor-memory loads, stores, barriers)
+//               are covered by the arithmetic of the other.  A warp has a tensor-memory
+//               quadrant and 128 columns, in two parts of 64 that it reads into registers at
+//               once; the second part's read releases the accumulator.  Output chunks of
+//               32 x 32 go through a swizzled staging tile and a TMA store; with a residual,
+//               its chunk is loaded into the same staging tile beforehand.
 // int8 accumulators are two full 256-column buffers; FP4 ones share 64 columns ([0, 256) and
 // [192, 448)) to leave room for the scale ring at [448, 508).
 //
@@ -47,12 +48,12 @@ constexpr int PS_OP = PROWS * PKB;            // 16 KiB: A, and B
 constexpr int PS_SFA = 4 * 512;
 constexpr int PS_SFB = 8 * 512;
 constexpr int P_STG = 32 * 64;                // one 32 x 32 bf16 staging tile; two per warp
-constexpr int P_COLS = 64 * 4 + 64 * 4;       // a warp's column scales (int8) and bias, fp32
 constexpr int P_GROUP = 8;                    // row blocks of a supertile
 template <bool I8>
 struct PairSmem {
     static constexpr int STAGE = 2 * PS_OP + (I8 ? 0 : PS_SFA + PS_SFB);
-    static constexpr int BYTES = 1024 + PSTAGES * STAGE + PEPI * (2 * P_STG + P_COLS) + 512;
+    static constexpr int COLS = (I8 ? 2 : 1) * 128 * 4;   // a warp's bias and column scales (int8)
+    static constexpr int BYTES = 1024 + PSTAGES * STAGE + PEPI * (2 * P_STG + COLS) + 512;
 };
 static_assert(PairSmem<false>::BYTES <= 232448 && PairSmem<true>::BYTES <= 232448,
               "dynamic shared memory above the 227 KiB a CTA can have");
@@ -194,7 +195,10 @@ __device__ __forceinline__ void pair_coords(const PairParams& p, int tile, int& 
     m_blk = super * P_GROUP + rest - n_blk * min(rows, P_GROUP);
 }
 
-template <bool I8, int ACT, bool GATED>
+// RES: a residual that TMA can load (n_out % 8 == 0).  A build of its own: tested per value
+// instead, its predicated-off loads, unpacking and additions were a quarter of the
+// instructions of a call without one.
+template <bool I8, int ACT, bool GATED, bool RES>
 __global__ void __launch_bounds__(PTHREADS, 1)
 gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
@@ -206,7 +210,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                                                ~uintptr_t(1023));
     uint8_t* sStg = smem + PSTAGES * SM::STAGE;
     uint8_t* sCols = sStg + PEPI * 2 * P_STG;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sCols + PEPI * P_COLS);   // used in the leader
+    uint64_t* full = reinterpret_cast<uint64_t*>(sCols + PEPI * SM::COLS);   // used in the leader
     uint64_t* empty = full + PSTAGES;
     uint64_t* acc_full = empty + PSTAGES;    // [2]
     uint64_t* acc_free = acc_full + 2;       // [2], used in the leader
@@ -228,7 +232,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_free[b], 2 * PEPI);
+            mbar_init(&acc_free[b], PEPI);          // a group of both CTAs
         }
         mbar_init(ovl_free, 2 * PEPI / 4);
         mbar_init(drain, 1);
@@ -372,16 +376,21 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         __syncwarp();
     } else {
         const int e = warp - 2;
+        const int group = e >> 3;                // tiles group, group + 2, ... of the pair
         const int quad = warp & 3;               // tensor-memory lanes 32 quad .. + 31
-        const int quarter = e >> 2;              // columns 64 quarter .. + 63
+        const int half = (e >> 2) & 1;           // columns 128 half .. + 127
         uint8_t* stg = sStg + e * 2 * P_STG;
-        float* ssw = reinterpret_cast<float*>(sCols + e * P_COLS);   // 64 column scales (int8)
-        float* sbias = ssw + 64;                                     // 64 bias values
+        float* sbias = reinterpret_cast<float*>(sCols + e * SM::COLS);   // 128 bias values
+        float* ssw = sbias + 128;                                        // 128 column scales (int8)
         uint64_t* rfull = res_full + 2 * e;
-        const uint32_t free0 = dsmem_addr(smem_u32(acc_free), 0);
+        const int b = group;                     // this group's accumulator buffer
+        const uint32_t free_b = dsmem_addr(smem_u32(&acc_free[b]), 0);
         const uint32_t ovl0 = dsmem_addr(smem_u32(ovl_free), 0);
+        // The columns that the FP4 buffers share are buffer 0's last 64 and buffer 1's first:
+        // their owners read that part first.
+        const int part0 = (!I8 && b == 0 && half == 1) ? 1 : 0;
+        const bool owns_shared = !I8 && half == 1 - b;
         const float alpha = I8 ? 0.0f : *p.alpha;
-        const bool res_tma = p.residual && p.tma_store;
         uint32_t res_phase = 0, res_ahead = 0;   // per staging tile: parity; loaded, not used
         // Loads the residual chunks of the warp's part of a tile (rows from row, columns from
         // n0) into the staging tiles that its output will take: chunk c in staging tile c (one
@@ -398,46 +407,51 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 res_ahead |= 1u << c;
             }
         };
-        // This lane's two columns of a tile (scale, bias) and its row's scale, fetched a tile
+        // This lane's four columns of a tile (bias, scale) and its row's scale, fetched a tile
         // ahead.  Columns past N repeat the last one; they are not stored.
-        float2 sw2 = make_float2(0.0f, 0.0f), bias2 = make_float2(0.0f, 0.0f);
+        float4 sw4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), bias4 = sw4;
         float row_scale = alpha;
         auto fetch_columns = [&](int row, int n0) {
-            const int n = n0 + 2 * lane;
+            const int n = n0 + 4 * lane;
+            const bool whole = n + 4 <= p.N;
             if (p.bias) {
-                const uint32_t w = n + 2 <= p.N ? *reinterpret_cast<const uint32_t*>(p.bias + n)
-                                                : (uint32_t)p.bias[min(n, p.N - 1)] |
-                                                      ((uint32_t)p.bias[min(n + 1, p.N - 1)] << 16);
-                bias2 = make_float2(bf16lo(w), bf16hi(w));
+                uint2 w;
+                if (whole) {
+                    w = *reinterpret_cast<const uint2*>(p.bias + n);
+                } else {
+                    w.x = (uint32_t)p.bias[min(n, p.N - 1)] | ((uint32_t)p.bias[min(n + 1, p.N - 1)] << 16);
+                    w.y = (uint32_t)p.bias[min(n + 2, p.N - 1)] | ((uint32_t)p.bias[min(n + 3, p.N - 1)] << 16);
+                }
+                bias4 = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
             }
             if constexpr (I8) {
-                sw2 = n + 2 <= p.N ? *reinterpret_cast<const float2*>(p.sw + n)
-                                   : make_float2(p.sw[min(n, p.N - 1)], p.sw[min(n + 1, p.N - 1)]);
+                if (whole) sw4 = *reinterpret_cast<const float4*>(p.sw + n);
+                else sw4 = make_float4(p.sw[min(n, p.N - 1)], p.sw[min(n + 1, p.N - 1)],
+                                       p.sw[min(n + 2, p.N - 1)], p.sw[min(n + 3, p.N - 1)]);
                 row_scale = row + lane < p.M ? p.sx[row + lane] : 0.0f;
             }
         };
-        int next_row = 0, next_n0 = 0;           // the warp's part of the next tile
+        int next_row = 0, next_n0 = 0;           // the warp's part of its next tile
         auto next_part = [&](int tile) {
             int m_blk, n_blk;
             pair_coords(p, tile, m_blk, n_blk);
             next_row = m_blk * 2 * PROWS + rank * PROWS + quad * 32;
-            next_n0 = n_blk * PN + quarter * 64;
+            next_n0 = n_blk * PN + half * 128;
         };
-        if (pair < p.tiles) {
-            next_part(pair);
-            if (res_tma) load_residual(next_row, next_n0);
+        const int first = pair + group * pairs, stride = 2 * pairs;
+        if (first < p.tiles) {
+            next_part(first);
+            if (RES) load_residual(next_row, next_n0 + 64 * part0);
             fetch_columns(next_row, next_n0);
         }
-        int it = 0;
+        uint32_t use = 0;
         bool ok = true;
-        for (int tile = pair; ok && tile < p.tiles; tile += pairs, ++it) {
-            const int b = it & 1;
-            const uint32_t use = (uint32_t)(it >> 1);
-            const int row0 = next_row, n0 = next_n0;
-            const bool more = tile + pairs < p.tiles;
+        for (int tile = first; ok && tile < p.tiles; tile += stride, ++use) {
+            const int row0 = next_row, tile_n0 = next_n0;
+            const bool more = tile + stride < p.tiles;
             __syncwarp();                        // the last tile's values have been read
-            if (I8) reinterpret_cast<float2*>(ssw)[lane] = sw2;
-            reinterpret_cast<float2*>(sbias)[lane] = bias2;
+            if (I8) reinterpret_cast<float4*>(ssw)[lane] = sw4;
+            reinterpret_cast<float4*>(sbias)[lane] = bias4;
             const float scale = row_scale;
             __syncwarp();
             if (!pair_wait_w(&acc_full[b], use & 1, abort_flag, p.status, p.budget_ns)) {
@@ -445,143 +459,148 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 break;
             }
             tc_fence_after();
-            uint32_t r[2][32];
-            const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + (b ? (I8 ? 256u : 192u) : 0u) +
-                                (uint32_t)(quarter * 64);
-            tmem_ld32(at, r[0]);
-            tmem_ld32(at + 32, r[1]);
-            tmem_ld_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                // buffer 0's last quarter and buffer 1's first are the shared columns
-                if (!I8 && quarter == (b ? 0 : 3)) arrive_cluster(ovl0);
-                arrive_cluster(free0 + 8u * (uint32_t)b);
-            }
-            if (more) {
-                next_part(tile + pairs);
-                fetch_columns(next_row, next_n0);
-            }
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                const int part = part0 ^ i;
+                const int n0 = tile_n0 + 64 * part;
+                uint32_t r[2][32];
+                const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + (b ? (I8 ? 256u : 192u) : 0u) +
+                                    (uint32_t)(half * 128 + part * 64);
+                tmem_ld32(at, r[0]);
+                tmem_ld32(at + 32, r[1]);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (i == 0 && owns_shared) arrive_cluster(ovl0);
+                    if (i == 1) arrive_cluster(free_b);
+                }
+                if (i == 0 && more) {
+                    next_part(tile + stride);
+                    fetch_columns(next_row, next_n0);
+                }
 
-            // Eight columns 8 g .. 8 g + 7 of chunk c: scale, bias, activation.
-            auto columns8 = [&](int c, int g, float (&v)[8]) {
-                const float4* b4 = reinterpret_cast<const float4*>(sbias) + 8 * c + 2 * g;
-                const float4* s4 = reinterpret_cast<const float4*>(ssw) + 8 * c + 2 * g;
+                // Eight columns 8 g .. 8 g + 7 of chunk c: scale, bias, activation.
+                auto columns8 = [&](int c, int g, float (&v)[8]) {
+                    const float4* b4 = reinterpret_cast<const float4*>(sbias) + 16 * part + 8 * c + 2 * g;
+                    const float4* s4 = reinterpret_cast<const float4*>(ssw) + 16 * part + 8 * c + 2 * g;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float4 bb = b4[q];
-                    float2 lo, hi;
-                    if constexpr (I8) {
-                        const float4 ss = s4[q];
-                        lo = make_float2(__int2float_rn((int)r[c][8 * g + 4 * q]),
-                                         __int2float_rn((int)r[c][8 * g + 4 * q + 1]));
-                        hi = make_float2(__int2float_rn((int)r[c][8 * g + 4 * q + 2]),
-                                         __int2float_rn((int)r[c][8 * g + 4 * q + 3]));
-                        lo = mul2_rn(mul2_rn(lo, make_float2(scale, scale)), make_float2(ss.x, ss.y));
-                        hi = mul2_rn(mul2_rn(hi, make_float2(scale, scale)), make_float2(ss.z, ss.w));
-                    } else {
-                        lo = make_float2(__uint_as_float(r[c][8 * g + 4 * q]),
-                                         __uint_as_float(r[c][8 * g + 4 * q + 1]));
-                        hi = make_float2(__uint_as_float(r[c][8 * g + 4 * q + 2]),
-                                         __uint_as_float(r[c][8 * g + 4 * q + 3]));
-                        lo = mul2_rn(lo, make_float2(scale, scale));
-                        hi = mul2_rn(hi, make_float2(scale, scale));
-                    }
-                    v[4 * q] = __fadd_rn(lo.x, bb.x);
-                    v[4 * q + 1] = __fadd_rn(lo.y, bb.y);
-                    v[4 * q + 2] = __fadd_rn(hi.x, bb.z);
-                    v[4 * q + 3] = __fadd_rn(hi.y, bb.w);
-                }
-                activate<ACT, GATED>(v);
-            };
-            // Output values 8 o .. 8 o + 7 of chunk c: one 8-column group, or, gated, the even
-            // places of two.
-            auto outputs8 = [&](int c, int o, float (&u)[8]) {
-                if constexpr (GATED) {
-                    float v[8];
-                    columns8(o >> 1, 2 * (o & 1), v);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) u[j] = v[2 * j];
-                    columns8(o >> 1, 2 * (o & 1) + 1, v);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) u[4 + j] = v[2 * j];
-                } else {
-                    columns8(c, o, u);
-                }
-            };
-            if (p.tma_store) {
-                bool stored = false;
-#pragma unroll
-                for (int c = 0; c < (GATED ? 1 : 2); ++c) {
-                    const int col = GATED ? n0 >> 1 : n0 + 32 * c;
-                    if (!ok || col >= p.n_out) continue;     // warp-uniform
-                    uint8_t* sb = stg + c * P_STG;
-                    if (res_tma) {
-                        ok = pair_wait_w(&rfull[c], (res_phase >> c) & 1, abort_flag, p.status, p.budget_ns);
-                        if (!ok) continue;
-                        res_phase ^= 1u << c;
-                        res_ahead &= ~(1u << c);
-                    }
-                    // 64-byte swizzle: 16-byte piece o of row r sits at o ^ ((r >> 1) & 3)
-#pragma unroll
-                    for (int o = 0; o < 4; ++o) {
-                        float u[8];
-                        outputs8(c, o, u);
-                        uint4* to = reinterpret_cast<uint4*>(sb + lane * 64 + ((o ^ ((lane >> 1) & 3)) << 4));
-                        uint32_t w[4];
-                        if (res_tma) {
-                            const uint4 t = *to;
-                            const uint32_t rw[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                u[2 * j] = __fadd_rn(u[2 * j], bf16lo(rw[j]));
-                                u[2 * j + 1] = __fadd_rn(u[2 * j + 1], bf16hi(rw[j]));
-                            }
-                        } else if (c == 0 && o == 0) {
-                            // the last tile's stores have read the staging tiles
-                            if (lane == 0) bulk_wait_read<0>();
-                            __syncwarp();
+                    for (int q = 0; q < 2; ++q) {
+                        const float4 bb = b4[q];
+                        float2 lo, hi;
+                        if constexpr (I8) {
+                            const float4 ss = s4[q];
+                            lo = make_float2(__int2float_rn((int)r[c][8 * g + 4 * q]),
+                                             __int2float_rn((int)r[c][8 * g + 4 * q + 1]));
+                            hi = make_float2(__int2float_rn((int)r[c][8 * g + 4 * q + 2]),
+                                             __int2float_rn((int)r[c][8 * g + 4 * q + 3]));
+                            lo = mul2_rn(mul2_rn(lo, make_float2(scale, scale)), make_float2(ss.x, ss.y));
+                            hi = mul2_rn(mul2_rn(hi, make_float2(scale, scale)), make_float2(ss.z, ss.w));
+                        } else {
+                            lo = make_float2(__uint_as_float(r[c][8 * g + 4 * q]),
+                                             __uint_as_float(r[c][8 * g + 4 * q + 1]));
+                            hi = make_float2(__uint_as_float(r[c][8 * g + 4 * q + 2]),
+                                             __uint_as_float(r[c][8 * g + 4 * q + 3]));
+                            lo = mul2_rn(lo, make_float2(scale, scale));
+                            hi = mul2_rn(hi, make_float2(scale, scale));
                         }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) w[j] = bf16x2_rn(u[2 * j], u[2 * j + 1]);
-                        *to = make_uint4(w[0], w[1], w[2], w[3]);
+                        v[4 * q] = __fadd_rn(lo.x, bb.x);
+                        v[4 * q + 1] = __fadd_rn(lo.y, bb.y);
+                        v[4 * q + 2] = __fadd_rn(hi.x, bb.z);
+                        v[4 * q + 3] = __fadd_rn(hi.y, bb.w);
                     }
-                    stored = true;
-                }
-                if (stored) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&tmY, stg, GATED ? n0 >> 1 : n0, row0);
-                        if (!GATED && n0 + 32 < p.n_out) tma_store_2d(&tmY, stg + P_STG, n0 + 32, row0);
-                        bulk_commit();
+                    activate<ACT, GATED>(v);
+                };
+                // Output values 8 o .. 8 o + 7 of chunk c: one 8-column group, or, gated, the even
+                // places of two.
+                auto outputs8 = [&](int c, int o, float (&u)[8]) {
+                    if constexpr (GATED) {
+                        float v[8];
+                        columns8(o >> 1, 2 * (o & 1), v);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) u[j] = v[2 * j];
+                        columns8(o >> 1, 2 * (o & 1) + 1, v);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) u[4 + j] = v[2 * j];
+                    } else {
+                        columns8(c, o, u);
                     }
-                }
-                if (ok && more && res_tma) {
-                    if (lane == 0) bulk_wait_read<0>();
-                    __syncwarp();
-                    load_residual(next_row, next_n0);
-                }
-            } else {
-                // rows of y are not 16-byte multiples: element by element
-                const int row = row0 + lane;
+                };
+                if (p.tma_store) {
+                    bool stored = false;
 #pragma unroll
-                for (int c = 0; c < (GATED ? 1 : 2); ++c)
+                    for (int c = 0; c < (GATED ? 1 : 2); ++c) {
+                        const int col = GATED ? n0 >> 1 : n0 + 32 * c;
+                        if (!ok || col >= p.n_out) continue;     // warp-uniform
+                        uint8_t* sb = stg + c * P_STG;
+                        if (RES) {
+                            ok = pair_wait_w(&rfull[c], (res_phase >> c) & 1, abort_flag, p.status, p.budget_ns);
+                            if (!ok) continue;
+                            res_phase ^= 1u << c;
+                            res_ahead &= ~(1u << c);
+                        }
+                        // 64-byte swizzle: 16-byte piece o of row r sits at o ^ ((r >> 1) & 3)
 #pragma unroll
-                    for (int o = 0; o < 4; ++o) {
-                        float u[8];
-                        outputs8(c, o, u);
-                        const int col = (GATED ? n0 >> 1 : n0 + 32 * c) + 8 * o;
-                        if (row >= p.M) continue;
-                        const size_t to = (size_t)row * p.n_out + col;
+                        for (int o = 0; o < 4; ++o) {
+                            float u[8];
+                            outputs8(c, o, u);
+                            uint4* to = reinterpret_cast<uint4*>(sb + lane * 64 + ((o ^ ((lane >> 1) & 3)) << 4));
+                            uint32_t w[4];
+                            if (RES) {
+                                const uint4 t = *to;
+                                const uint32_t rw[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (col + j < p.n_out) {
-                                if (p.residual)
-                                    u[j] = __fadd_rn(u[j], __uint_as_float((uint32_t)p.residual[to + j] << 16));
-                                p.y[to + j] = (uint16_t)bf16x2_rn(u[j], 0.0f);
+                                for (int j = 0; j < 4; ++j) {
+                                    u[2 * j] = __fadd_rn(u[2 * j], bf16lo(rw[j]));
+                                    u[2 * j + 1] = __fadd_rn(u[2 * j + 1], bf16hi(rw[j]));
+                                }
+                            } else if (c == 0 && o == 0) {
+                                // the last part's stores have read the staging tiles
+                                if (lane == 0) bulk_wait_read<0>();
+                                __syncwarp();
                             }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) w[j] = bf16x2_rn(u[2 * j], u[2 * j + 1]);
+                            *to = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                        stored = true;
                     }
+                    if (stored) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&tmY, stg, GATED ? n0 >> 1 : n0, row0);
+                            if (!GATED && n0 + 32 < p.n_out) tma_store_2d(&tmY, stg + P_STG, n0 + 32, row0);
+                            bulk_commit();
+                        }
+                    }
+                    if (ok && RES && (i == 0 || more)) {
+                        if (lane == 0) bulk_wait_read<0>();
+                        __syncwarp();
+                        if (i == 0) load_residual(row0, tile_n0 + 64 * (part0 ^ 1));
+                        else load_residual(next_row, next_n0 + 64 * part0);
+                    }
+                } else {
+                    // rows of y are not 16-byte multiples: element by element
+                    const int row = row0 + lane;
+#pragma unroll
+                    for (int c = 0; c < (GATED ? 1 : 2); ++c)
+#pragma unroll
+                        for (int o = 0; o < 4; ++o) {
+                            float u[8];
+                            outputs8(c, o, u);
+                            const int col = (GATED ? n0 >> 1 : n0 + 32 * c) + 8 * o;
+                            if (row >= p.M) continue;
+                            const size_t to = (size_t)row * p.n_out + col;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (col + j < p.n_out) {
+                                    if (p.residual)
+                                        u[j] = __fadd_rn(u[j], __uint_as_float((uint32_t)p.residual[to + j] << 16));
+                                    p.y[to + j] = (uint16_t)bf16x2_rn(u[j], 0.0f);
+                                }
+                        }
+                }
             }
         }
         // residual chunks still on their way must land before the block can exit
@@ -622,16 +641,22 @@ bool make_scale_map(CUtensorMap* map, const void* base, int64_t chunks) {
 using PairKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
                             CUtensorMap, PairParams);
 
+template <bool I8, bool GATED, bool RES>
+PairKernel pair_kernel_of(int base) {
+    static const PairKernel table[5] = {gemm_pair_kernel<I8, NVFP4_ACT_NONE, GATED, RES>,
+                                        gemm_pair_kernel<I8, NVFP4_ACT_RELU, GATED, RES>,
+                                        gemm_pair_kernel<I8, NVFP4_ACT_GELU, GATED, RES>,
+                                        gemm_pair_kernel<I8, NVFP4_ACT_GELU_TANH, GATED, RES>,
+                                        gemm_pair_kernel<I8, NVFP4_ACT_SILU, GATED, RES>};
+    return table[base];
+}
+
 template <bool I8>
-PairKernel pair_kernel(int activation) {
-    static const PairKernel table[2][5] = {
-        {gemm_pair_kernel<I8, NVFP4_ACT_NONE, false>, gemm_pair_kernel<I8, NVFP4_ACT_RELU, false>,
-         gemm_pair_kernel<I8, NVFP4_ACT_GELU, false>, gemm_pair_kernel<I8, NVFP4_ACT_GELU_TANH, false>,
-         gemm_pair_kernel<I8, NVFP4_ACT_SILU, false>},
-        {gemm_pair_kernel<I8, NVFP4_ACT_NONE, true>, gemm_pair_kernel<I8, NVFP4_ACT_RELU, true>,
-         gemm_pair_kernel<I8, NVFP4_ACT_GELU, true>, gemm_pair_kernel<I8, NVFP4_ACT_GELU_TANH, true>,
-         gemm_pair_kernel<I8, NVFP4_ACT_SILU, true>}};
-    return table[(activation & NVFP4_ACT_GATED) ? 1 : 0][activation & ~NVFP4_ACT_GATED];
+PairKernel pair_kernel(int activation, bool res) {
+    const int base = activation & ~NVFP4_ACT_GATED;
+    if (activation & NVFP4_ACT_GATED)
+        return res ? pair_kernel_of<I8, true, true>(base) : pair_kernel_of<I8, true, false>(base);
+    return res ? pair_kernel_of<I8, false, true>(base) : pair_kernel_of<I8, false, false>(base);
 }
 
 template <bool I8>
@@ -641,15 +666,6 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
     if (st != NVFP4_OK) return st;
     int* status = nullptr;
     if ((st = status_word(&status)) != NVFP4_OK) return st;
-    const PairKernel kernel = pair_kernel<I8>(g.epi.activation);
-    static std::atomic<int> attr_set[64][32];
-    std::atomic<int>& set = attr_set[dev.device & 63][g.epi.activation & 31];
-    if (!set.load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 PairSmem<I8>::BYTES) != cudaSuccess)
-            return NVFP4_ERR_CUDA;
-        set.store(1, std::memory_order_release);
-    }
     PairParams p{};
     const int64_t kbytes = I8 ? g.K : g.K / 2;
     p.alpha = g.alpha;
@@ -673,6 +689,16 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
     p.w_early = g.weights_ready ? 1 : 0;
     p.status = status;
     p.budget_ns = 4000000000ull;   // 4 s
+    const bool res = p.residual && p.tma_store;
+    const PairKernel kernel = pair_kernel<I8>(g.epi.activation, res);
+    static std::atomic<int> attr_set[64][2][32];
+    std::atomic<int>& set = attr_set[dev.device & 63][res][g.epi.activation & 31];
+    if (!set.load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 PairSmem<I8>::BYTES) != cudaSuccess)
+            return NVFP4_ERR_CUDA;
+        set.store(1, std::memory_order_release);
+    }
     CUtensorMap mapA, mapB, mapSFA, mapSFB, mapY, mapR;
     if (!make_operand_map(&mapA, g.a, g.M, kbytes, PROWS) ||
         !make_operand_map(&mapB, g.b, g.N, kbytes, PROWS))
@@ -687,8 +713,7 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
     }
     if (p.tma_store && !make_output_map(&mapY, g.y, g.M, p.n_out)) return NVFP4_ERR_CUDA;
     mapR = mapY;
-    if (p.tma_store && p.residual &&
-        !make_output_map(&mapR, const_cast<void*>(g.epi.residual), g.M, p.n_out))
+    if (res && !make_output_map(&mapR, const_cast<void*>(g.epi.residual), g.M, p.n_out))
         return NVFP4_ERR_CUDA;
 
     const int pairs = p.tiles < dev.sms / 2 ? p.tiles : dev.sms / 2;
@@ -715,9 +740,14 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
 }  // namespace
 
 nvfp4_status launch_gemm_act(const GemmActArgs& g, cudaStream_t stream) {
+    DeviceInfo dev;
+    nvfp4_status st = device_info(&dev);
+    if (st != NVFP4_OK) return st;
+    const bool long_weight = (g.N + 255) / 256 * 2 > dev.sms;   // no cluster left to split K over
+    if (g.M <= kStreamMaxRows && long_weight) return launch_gemm_stream(g, stream);
     if (g.M <= kSmallMaxRows) return launch_gemm_small_act(g, stream);
     bool taken = false;
-    const nvfp4_status st = launch_gemm_act_split_k(g, &taken, stream);
+    st = launch_gemm_act_split_k(g, &taken, stream);
     if (st != NVFP4_OK || taken) return st;
     return g.int8 ? launch_pair_impl<true>(g, stream) : launch_pair_impl<false>(g, stream);
 }

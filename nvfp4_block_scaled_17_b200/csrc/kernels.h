@@ -138,6 +138,8 @@ struct GemmActArgs {
 // grids of few tiles (taken says whether it was launched), SM pairs for the rest.
 nvfp4_status launch_gemm_act(const GemmActArgs& g, cudaStream_t stream);
 nvfp4_status launch_gemm_small_act(const GemmActArgs& g, cudaStream_t stream);
+constexpr int64_t kStreamMaxRows = 128;
+nvfp4_status launch_gemm_stream(const GemmActArgs& g, cudaStream_t stream);
 nvfp4_status launch_gemm_act_split_k(const GemmActArgs& g, bool* taken, cudaStream_t stream);
 
 // bf16 [M, N] tensor map with a 32 x 32 box and 64-byte swizzle (N % 8 == 0).

@@ -278,3 +278,42 @@ def test_block_in_a_graph(kind, M):
         torch.cuda.synchronize()
         for _, _, r, _ in graphs:
             assert torch.equal(r.view(torch.int16), want[i].view(torch.int16))
+
+
+@pytest.mark.parametrize("kind", ["int8", "nvfp4"])
+@pytest.mark.parametrize("M", [1, 16, 17, 128])
+@pytest.mark.parametrize("N,K", [(19200, 320), (38038, 64), (25602, 1152)])
+def test_long_weights(kind, M, N, K):
+    """Few rows against a weight with more row blocks than SMs."""
+    one(kind, M, N, K, "silu", True, True, True, prepared=True)
+    one(kind, M, N, K, "gelu", False, False, True)
+    one(kind, M, N, K, "none", True, True, False)
+
+
+@pytest.mark.parametrize("kind", ["int8", "nvfp4"])
+def test_linear_act_weights_written_just_before(kind):
+    """The linears may load their weight before the activation quantizer has ended; weights
+    that the stream wrote just before the call have to be seen."""
+    for rows, N, K in ((1, 19456, 512), (200, 19456, 512), (1, 512, 2048), (100, 512, 2048)):
+        g = W._gen(rows + N, DEV)
+        x = W.normal((rows, K), 1.0, g, DEV).to(BF16)
+        ws = [W.normal((N, K), 0.05, g, DEV).to(BF16) for _ in range(3)]
+        if kind == "int8":
+            packs = [nv.int8_quantize_rows(w) for w in ws]
+        else:
+            packs = [nv.pack_weight(w) for w in ws]
+        live = tuple(t.clone() for t in packs[0])
+
+        def call():
+            if kind == "int8":
+                return nv.int8_linear_act(x, *live, activation="gelu")
+            return nv.nvfp4_linear_act(x, *live, N, activation="gelu")
+
+        for k in (1, 2, 0):
+            for t, s in zip(live, packs[k]):
+                t.copy_(s)
+            y = call()
+            torch.cuda.synchronize()
+            ref = (nv.int8_linear_act(x, *packs[k], activation="gelu") if kind == "int8"
+                   else nv.nvfp4_linear_act(x, *packs[k], N, activation="gelu"))
+            assert torch.equal(y.view(torch.int16), ref.view(torch.int16))
