@@ -317,3 +317,13 @@ def test_linear_act_weights_written_just_before(kind):
             ref = (nv.int8_linear_act(x, *packs[k], activation="gelu") if kind == "int8"
                    else nv.nvfp4_linear_act(x, *packs[k], N, activation="gelu"))
             assert torch.equal(y.view(torch.int16), ref.view(torch.int16))
+
+
+@pytest.mark.parametrize("kind", ["int8", "nvfp4"])
+@pytest.mark.parametrize("M,N,K", [(64, 1030, 2560), (512, 1024, 5120), (130, 260, 1280),
+                                   (300, 520, 2624)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_split_k(kind, M, N, K, gated):
+    """Few tiles of a long K: clusters that share it."""
+    one(kind, M, N, K, "silu", gated, True, True, prepared=True)
+    one(kind, M, N, K, "gelu", gated, False, False)
