@@ -23,6 +23,8 @@
 //               once; the second part's read releases the accumulator.  Output chunks of
 //               32 x 32 go through a swizzled staging tile and a TMA store; with a residual,
 //               its chunk is loaded into the same staging tile beforehand.
+// The tiles of a last, at most half full wave are cut into two of 128 columns each, which
+// then all run at once: 4096 x 5120 x 25600 is 320 tiles on 74 pairs, 4.5 waves instead of 5.
 // int8 accumulators are two full 256-column buffers; FP4 ones share 64 columns ([0, 256) and
 // [192, 448)) to leave room for the scale ring at [448, 508).
 //
@@ -33,6 +35,7 @@
 #include "kernels.h"
 
 #include <atomic>
+#include <type_traits>
 
 namespace nvfp4 {
 
@@ -63,6 +66,7 @@ constexpr int PSF_SLOTS = 5;
 // N = 256, M = 256 over the pair
 constexpr uint32_t PIDESC = (1u << 7) | (1u << 10) | ((uint32_t)(PN >> 3) << 17) | (16u << 24);
 constexpr uint32_t PIDESC_I8 = PIDESC | (2u << 4);
+constexpr uint32_t PIDESC_HALF = (uint32_t)(PN >> 4) << 17;   // N = 128: subtracted
 
 struct PairParams {
     const float* alpha;
@@ -72,7 +76,8 @@ struct PairParams {
     const uint16_t* residual;  // bf16 [M, n_out] or null
     uint16_t* y;               // bf16 [M, n_out]
     int M, N, n_out;
-    int m_blocks, n_blocks, tiles;
+    int m_blocks, n_blocks;
+    int items, whole;          // work items: whole tiles, then halves of the tiles after them
     FastDiv div_super, div_last;   // by the tiles of a supertile, by the last one's rows
     int k_tiles;               // stages of K
     int kchunks;               // 32-byte K steps
@@ -113,6 +118,7 @@ __device__ __forceinline__ void commit_own_w(uint64_t* bar) {
         : "memory");
 }
 
+template <bool HALF>
 __device__ __forceinline__ void pair_step_i8_w(uint32_t d, uint64_t ad, uint64_t bd,
                                                uint32_t accumulate) {
     asm volatile(
@@ -120,15 +126,31 @@ __device__ __forceinline__ void pair_step_i8_w(uint32_t d, uint64_t ad, uint64_t
         "setp.ne.b32 p, %4, 0;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(PIDESC_I8), "r"(accumulate)
+        "l"(ad), "l"(bd), "r"(HALF ? PIDESC_I8 - PIDESC_HALF : PIDESC_I8), "r"(accumulate)
         : "memory");
 }
 
-// One FP4 K step: each SM's scale chunks (its A rows; both halves of B) from its own shared
-// memory into its own tensor memory, then the MMA over both.
+// One FP4 K step: each SM's scale chunks (its A rows; the one or two 128-row halves of B) from
+// its own shared memory into its own tensor memory, then the MMA over both.
+template <bool HALF>
 __device__ __forceinline__ void pair_step_fp4_w(uint32_t d, uint64_t ad, uint64_t bd, uint32_t sf_t,
                                                 uint64_t sfa_d, uint64_t sfb_d,
                                                 uint32_t accumulate) {
+    if constexpr (HALF) {
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t.reg .b32 t;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "add.u32 t, %5, 4;\n\t"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%5], %6;\n\t"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t], %7;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, "
+            "[%5], [t], p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(PIDESC - PIDESC_HALF), "r"(accumulate), "r"(sf_t), "l"(sfa_d),
+            "l"(sfb_d)
+            : "memory");
+        return;
+    }
     asm volatile(
         "{\n\t.reg .pred p, e;\n\t.reg .b32 t, u;\n\t.reg .b64 s;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
@@ -187,12 +209,19 @@ __device__ __forceinline__ bool pair_wait_w(uint64_t* bar, uint32_t parity, vola
 // Tile order: supertiles of eight row blocks, walked column block by column block, so the
 // 74 tiles in flight share about as many panels of A as of B (8192^3 int8: 685 MB of DRAM
 // reads when they walked whole rows of tiles, the operands being 134 MB).
-__device__ __forceinline__ void pair_coords(const PairParams& p, int tile, int& m_blk, int& n_blk) {
+struct Item {
+    int m_blk, n0;             // row block; first column
+    bool half;                 // 128 columns instead of 256
+};
+__device__ __forceinline__ Item pair_item(const PairParams& p, int item) {
+    const bool half = item >= p.whole;
+    const int tile = half ? p.whole + ((item - p.whole) >> 1) : item;
     const int super = (int)fast_div((uint32_t)tile, p.div_super);
     const int rest = tile - super * P_GROUP * p.n_blocks;
     const int rows = p.m_blocks - super * P_GROUP;
-    n_blk = rows >= P_GROUP ? rest / P_GROUP : (int)fast_div((uint32_t)rest, p.div_last);
-    m_blk = super * P_GROUP + rest - n_blk * min(rows, P_GROUP);
+    const int n_blk = rows >= P_GROUP ? rest / P_GROUP : (int)fast_div((uint32_t)rest, p.div_last);
+    const int m_blk = super * P_GROUP + rest - n_blk * min(rows, P_GROUP);
+    return {m_blk, n_blk * PN + (half ? ((item - p.whole) & 1) * (PN / 2) : 0), half};
 }
 
 // RES: a residual that TMA can load (n_out % 8 == 0).  A build of its own: tested per value
@@ -201,9 +230,9 @@ __device__ __forceinline__ void pair_coords(const PairParams& p, int tile, int& 
 template <bool I8, int ACT, bool GATED, bool RES>
 __global__ void __launch_bounds__(PTHREADS, 1)
 gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
-                 const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmR,
-                 const PairParams p) {
+                 const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmSFA,
+                 const __grid_constant__ CUtensorMap tmSFB, const __grid_constant__ CUtensorMap tmY,
+                 const __grid_constant__ CUtensorMap tmR, const PairParams p) {
     using SM = PairSmem<I8>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -253,22 +282,28 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 
     // Producer: one stage's B side (box and scales) and A side.
     const uint32_t full0 = dsmem_addr(smem_u32(full), 0);    // the leader's full barriers
-    auto load_b = [&](int stage, int kt, int n_blk) {
+    auto load_b = [&](int stage, int kt, const Item& w) {
         const uint32_t s = smem_u32(smem + stage * SM::STAGE), bar = full0 + 8u * (uint32_t)stage;
-        tma_load_2d_pair_w(s + PS_OP, &tmB, bar, kt * PKB, n_blk * PN + rank * PROWS);
+        const uint32_t sf = s + 2 * PS_OP + PS_SFA;
+        if (w.half) tma_load_2d_pair_w(s + PS_OP, &tmBh, bar, kt * PKB, w.n0 + rank * (PROWS / 2));
+        else tma_load_2d_pair_w(s + PS_OP, &tmB, bar, kt * PKB, w.n0 + rank * PROWS);
         if constexpr (!I8) {
-            // 512-byte scale chunks of the tile's two 128-row halves, four K steps each
-            const int at = p.prepared ? (n_blk * p.k_tiles + kt) * 8 : 2 * n_blk * p.kchunks + 4 * kt;
-            const int second = p.prepared ? 4 : p.kchunks;
-            tma_load_2d_pair_w(s + 2 * PS_OP + PS_SFA, &tmSFB, bar, 0, at);
-            tma_load_2d_pair_w(s + 2 * PS_OP + PS_SFA + 2048, &tmSFB, bar, 0, at + second);
+            // 512-byte scale chunks of the tile's 128-row halves, four K steps each
+            const int h = w.n0 >> 7, n_blk = w.n0 >> 8;
+            const int at = p.prepared ? (n_blk * p.k_tiles + kt) * 8 + (h & 1) * 4 : h * p.kchunks + 4 * kt;
+            tma_load_2d_pair_w(sf, &tmSFB, bar, 0, at);
+            if (!w.half) tma_load_2d_pair_w(sf + 2048, &tmSFB, bar, 0, at + (p.prepared ? 4 : p.kchunks));
         }
     };
-    auto load_a = [&](int stage, int kt, int m_blk) {
+    auto load_a = [&](int stage, int kt, const Item& w) {
         const uint32_t s = smem_u32(smem + stage * SM::STAGE), bar = full0 + 8u * (uint32_t)stage;
-        tma_load_2d_pair_w(s, &tmA, bar, kt * PKB, m_blk * 2 * PROWS + rank * PROWS);
+        tma_load_2d_pair_w(s, &tmA, bar, kt * PKB, w.m_blk * 2 * PROWS + rank * PROWS);
         if constexpr (!I8)
-            tma_load_2d_pair_w(s + 2 * PS_OP, &tmSFA, bar, 0, (2 * m_blk + rank) * p.kchunks + 4 * kt);
+            tma_load_2d_pair_w(s + 2 * PS_OP, &tmSFA, bar, 0, (2 * w.m_blk + rank) * p.kchunks + 4 * kt);
+    };
+    // both CTAs' bytes of a stage
+    auto stage_bytes = [&](const Item& w) -> uint32_t {
+        return 2u * (SM::STAGE - (w.half ? PS_OP / 2 + (I8 ? 0 : PS_SFB / 2) : 0));
     };
     int n_early = 0;
     if (warp == 0) {
@@ -276,13 +311,12 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             prefetch_tensormap(&tmA);
             prefetch_tensormap(&tmB);
         }
-        if (p.w_early && pair < p.tiles) {
-            int m_blk, n_blk;
-            pair_coords(p, pair, m_blk, n_blk);
+        if (p.w_early && pair < p.items) {
+            const Item w = pair_item(p, pair);
             n_early = min(PSTAGES, p.k_tiles);
             for (int i = 0; i < n_early; ++i) {
-                if (rank == 0) mbar_arrive_expect_tx_w(&full[i], 2 * SM::STAGE);
-                load_b(i, i, n_blk);
+                if (rank == 0) mbar_arrive_expect_tx_w(&full[i], stage_bytes(w));
+                load_b(i, i, w);
             }
         }
     }
@@ -293,9 +327,8 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         int stage = 0, fills = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int tile = pair; ok && tile < p.tiles; tile += pairs) {
-            int m_blk, n_blk;
-            pair_coords(p, tile, m_blk, n_blk);
+        for (int item = pair; ok && item < p.items; item += pairs) {
+            const Item w = pair_item(p, item);
             for (int kt = 0; kt < p.k_tiles; ++kt, ++fills) {
                 if (fills >= n_early) {
                     if (!pair_wait_w(&empty[stage], phase ^ 1, abort_flag, p.status,
@@ -303,10 +336,10 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         ok = false;
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx_w(&full[stage], 2 * SM::STAGE);
-                    load_b(stage, kt, n_blk);
+                    if (rank == 0) mbar_arrive_expect_tx_w(&full[stage], stage_bytes(w));
+                    load_b(stage, kt, w);
                 }
-                load_a(stage, kt, m_blk);
+                load_a(stage, kt, w);
                 if (++stage == PSTAGES) {
                     stage = 0;
                     phase ^= 1;
@@ -324,7 +357,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             int stage = 0, it = 0, sf_slot = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int tile = pair; ok && tile < p.tiles; tile += pairs, ++it) {
+            for (int item = pair; ok && item < p.items; item += pairs, ++it) {
                 const int b = it & 1;
                 const uint32_t use = (uint32_t)(it >> 1);
                 if (!pair_wait_w(&acc_free[b], (use & 1) ^ 1, abort_flag, p.status, p.budget_ns) ||
@@ -335,36 +368,44 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 }
                 tc_fence_after();
                 const uint32_t acc = tmem + (b ? (I8 ? 256u : 192u) : 0u);
-                for (int kt = 0; kt < p.k_tiles; ++kt) {
-                    if (!pair_wait_w(&full[stage], phase, abort_flag, p.status, p.budget_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const int steps = min(4, p.kchunks - 4 * kt);
-                    const uint32_t s = smem_u32(smem + stage * SM::STAGE);
-                    const uint64_t ad = sdesc_kmajor_sw128(s), bd = sdesc_kmajor_sw128(s + PS_OP);
-                    const uint64_t sad = sdesc_sf(s + 2 * PS_OP), sbd = sdesc_sf(s + 2 * PS_OP + PS_SFA);
+                // One loop for each width: a choice inside it costs the issue of every MMA (8192^3
+                // FP4 245 us, 306 with a branch per K step).
+                auto mainloop = [&](auto width) {
+                    constexpr bool HALF = decltype(width)::value;
+                    for (int kt = 0; kt < p.k_tiles; ++kt) {
+                        if (!pair_wait_w(&full[stage], phase, abort_flag, p.status, p.budget_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const int steps = min(4, p.kchunks - 4 * kt);
+                        const uint32_t s = smem_u32(smem + stage * SM::STAGE);
+                        const uint64_t ad = sdesc_kmajor_sw128(s), bd = sdesc_kmajor_sw128(s + PS_OP);
+                        const uint64_t sad = sdesc_sf(s + 2 * PS_OP);
+                        const uint64_t sbd = sdesc_sf(s + 2 * PS_OP + PS_SFA);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (kk < steps) {
-                            const uint32_t accumulate = (kt > 0 || kk > 0) ? 1u : 0u;
-                            if constexpr (I8) {
-                                pair_step_i8_w(acc, ad + 2 * kk, bd + 2 * kk, accumulate);
-                            } else {
-                                pair_step_fp4_w(acc, ad + 2 * kk, bd + 2 * kk,
-                                                tmem + PTMEM_SF + 12u * (uint32_t)sf_slot,
-                                                sad + 32 * kk, sbd + 32 * kk, accumulate);
-                                sf_slot = sf_slot == PSF_SLOTS - 1 ? 0 : sf_slot + 1;
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if (kk < steps) {
+                                const uint32_t accumulate = (kt > 0 || kk > 0) ? 1u : 0u;
+                                if constexpr (I8) {
+                                    pair_step_i8_w<HALF>(acc, ad + 2 * kk, bd + 2 * kk, accumulate);
+                                } else {
+                                    pair_step_fp4_w<HALF>(acc, ad + 2 * kk, bd + 2 * kk,
+                                                          tmem + PTMEM_SF + 12u * (uint32_t)sf_slot,
+                                                          sad + 32 * kk, sbd + 32 * kk, accumulate);
+                                    sf_slot = sf_slot == PSF_SLOTS - 1 ? 0 : sf_slot + 1;
+                                }
                             }
                         }
+                        commit_both_w(&empty[stage]);
+                        if (++stage == PSTAGES) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
                     }
-                    commit_both_w(&empty[stage]);
-                    if (++stage == PSTAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                }
+                };
+                if (item >= p.whole) mainloop(std::true_type{});
+                else mainloop(std::false_type{});
                 if (!ok) break;
                 commit_both_w(&acc_full[b]);
             }
@@ -432,23 +473,23 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             }
         };
         int next_row = 0, next_n0 = 0;           // the warp's part of its next tile
-        auto next_part = [&](int tile) {
-            int m_blk, n_blk;
-            pair_coords(p, tile, m_blk, n_blk);
-            next_row = m_blk * 2 * PROWS + rank * PROWS + quad * 32;
-            next_n0 = n_blk * PN + half * 128;
+        auto next_part = [&](int item) {
+            const Item w = pair_item(p, item);
+            next_row = w.m_blk * 2 * PROWS + rank * PROWS + quad * 32;
+            // half an item has no columns for the second half's warps
+            next_n0 = half == 0 ? w.n0 : w.half ? p.N : w.n0 + 128;
         };
         const int first = pair + group * pairs, stride = 2 * pairs;
-        if (first < p.tiles) {
+        if (first < p.items) {
             next_part(first);
             if (RES) load_residual(next_row, next_n0 + 64 * part0);
             fetch_columns(next_row, next_n0);
         }
         uint32_t use = 0;
         bool ok = true;
-        for (int tile = first; ok && tile < p.tiles; tile += stride, ++use) {
+        for (int item = first; ok && item < p.items; item += stride, ++use) {
             const int row0 = next_row, tile_n0 = next_n0;
-            const bool more = tile + stride < p.tiles;
+            const bool more = item + stride < p.items;
             __syncwarp();                        // the last tile's values have been read
             if (I8) reinterpret_cast<float4*>(ssw)[lane] = sw4;
             reinterpret_cast<float4*>(sbias)[lane] = bias4;
@@ -476,7 +517,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     if (i == 1) arrive_cluster(free_b);
                 }
                 if (i == 0 && more) {
-                    next_part(tile + stride);
+                    next_part(item + stride);
                     fetch_columns(next_row, next_n0);
                 }
 
@@ -639,7 +680,7 @@ bool make_scale_map(CUtensorMap* map, const void* base, int64_t chunks) {
 }
 
 using PairKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
-                            CUtensorMap, PairParams);
+                            CUtensorMap, CUtensorMap, PairParams);
 
 template <bool I8, bool GATED, bool RES>
 PairKernel pair_kernel_of(int base) {
@@ -679,7 +720,10 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
     p.n_out = (int)((g.epi.activation & NVFP4_ACT_GATED) ? g.N / 2 : g.N);
     p.m_blocks = (int)((g.M + 2 * PROWS - 1) / (2 * PROWS));
     p.n_blocks = (int)((g.N + PN - 1) / PN);
-    p.tiles = p.m_blocks * p.n_blocks;
+    const int tiles = p.m_blocks * p.n_blocks, max_pairs = dev.sms / 2;
+    const int last = tiles % max_pairs;        // tiles of the last wave
+    p.whole = 2 * last <= max_pairs ? tiles - last : tiles;
+    p.items = p.whole + 2 * (tiles - p.whole);
     p.div_super = make_fastdiv((uint32_t)(P_GROUP * p.n_blocks));
     p.div_last = make_fastdiv((uint32_t)(p.m_blocks % P_GROUP ? p.m_blocks % P_GROUP : P_GROUP));
     p.k_tiles = (int)((kbytes + PKB - 1) / PKB);
@@ -699,9 +743,10 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
             return NVFP4_ERR_CUDA;
         set.store(1, std::memory_order_release);
     }
-    CUtensorMap mapA, mapB, mapSFA, mapSFB, mapY, mapR;
+    CUtensorMap mapA, mapB, mapBh, mapSFA, mapSFB, mapY, mapR;
     if (!make_operand_map(&mapA, g.a, g.M, kbytes, PROWS) ||
-        !make_operand_map(&mapB, g.b, g.N, kbytes, PROWS))
+        !make_operand_map(&mapB, g.b, g.N, kbytes, PROWS) ||
+        !make_operand_map(&mapBh, g.b, g.N, kbytes, PROWS / 2))
         return NVFP4_ERR_CUDA;
     mapSFA = mapSFB = mapY = mapA;             // where unused
     if (!I8) {
@@ -716,7 +761,7 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
     if (res && !make_output_map(&mapR, const_cast<void*>(g.epi.residual), g.M, p.n_out))
         return NVFP4_ERR_CUDA;
 
-    const int pairs = p.tiles < dev.sms / 2 ? p.tiles : dev.sms / 2;
+    const int pairs = p.items < max_pairs ? p.items : max_pairs;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
     cfg.blockDim = dim3(PTHREADS, 1, 1);
@@ -731,7 +776,7 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, mapA, mapB, mapSFA, mapSFB, mapY, mapR, p) ==
+    return cudaLaunchKernelEx(&cfg, kernel, mapA, mapB, mapBh, mapSFA, mapSFB, mapY, mapR, p) ==
                    cudaSuccess
                ? NVFP4_OK
                : NVFP4_ERR_CUDA;
