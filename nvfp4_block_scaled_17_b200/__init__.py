@@ -6,7 +6,8 @@ Every function here marshals arguments and calls the same-named entry point of
 ``libnvfp4_b200.so`` (declared in ``include/nvfp4.h``); all arithmetic runs in
 that library's CUDA kernels.  PyTorch only provides device memory and the current
 stream.  There is no CPU fallback: if the library is missing or the device is not
-a B200, the calls raise.
+a B200, the calls raise.  Most calls are marshalled by ctypes; those of the norms and of the
+products with an epilogue, which serve single tokens, by a small extension module.
 """
 from __future__ import annotations
 
@@ -95,8 +96,29 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+# the entry points that the compiled part of the binding calls, in the order it takes them
+_BOUND = ("int8_rmsnorm_quantize", "nvfp4_rmsnorm_quantize", "int8_gemm_act", "nvfp4_gemm_act",
+          "int8_linear_act", "nvfp4_linear_act", "nvfp4_scale_bytes", "nvfp4_prepared_scale_bytes")
+_bound = None
+
+
+def _calls():
+    """The compiled argument checks and calls (csrc/binding.cpp), bound to the loaded library."""
+    global _bound
+    if _bound is None:
+        L = lib()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("the binding's extension module is missing: build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        _binding.set_entries(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _BOUND))
+        _bound = _binding
+    return _bound
+
+
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
@@ -127,37 +149,6 @@ def _scalar(t, device, name):
     if t.dtype != torch.float32 or t.numel() != 1 or not t.is_cuda:
         raise TypeError(f"{name} must be a one-element CUDA float32 tensor")
     return t
-
-
-def _need(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype,
-          device: torch.device) -> int | None:
-    """The address of a tensor argument that has to be exactly this (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.device != device:
-        raise TypeError(f"{name} must be a {dtype} tensor on {device}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
-    return t.data_ptr()
-
-
-def _need_bytes(t: torch.Tensor, name: str, least: int, device: torch.device) -> int:
-    """The address of a packed uint8 buffer of at least `least` bytes."""
-    if t.dtype is not torch.uint8 or t.device != device:
-        raise TypeError(f"{name} must be a torch.uint8 tensor on {device}")
-    if t.numel() < least or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous and hold at least {least} bytes")
-    return t.data_ptr()
-
-
-def _here(t: torch.Tensor, name: str) -> torch.device:
-    """The device of a call's first tensor, which has to be the current one: the library
-    launches on the current device."""
-    if not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    return t.device
 
 
 # ---------------------------------------------------------------------------
@@ -367,30 +358,6 @@ def int8_linear(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
 # norm in front of a quantized linear
 # ---------------------------------------------------------------------------
 
-def _norm_inputs(x, weight, residual, residual_out, norm_out):
-    """(device, residual_out, input addresses, output addresses) of a norm call."""
-    dev = _here(x, "x")
-    _bf16_2d(x, "x")
-    shape = x.shape
-    x_ptr = x.data_ptr()
-    r_ptr = _need(residual, "residual", shape, torch.bfloat16, dev)
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out needs a residual")
-    elif residual_out is None:
-        residual_out = torch.empty_like(x)
-    h_ptr = _need(residual_out, "residual_out", shape, torch.bfloat16, dev)
-    n_ptr = _need(norm_out, "norm_out", shape, torch.bfloat16, dev)
-    size = 2 * x.numel()
-    if h_ptr is not None and (0 < abs(h_ptr - x_ptr) < size or 0 < abs(h_ptr - r_ptr) < size):
-        raise ValueError("residual_out must be x or residual itself or not overlap them")
-    if n_ptr is not None and any(p is not None and abs(n_ptr - p) < size
-                                 for p in (x_ptr, r_ptr, h_ptr)):
-        raise ValueError("norm_out must not overlap the other tensors")
-    return dev, residual_out, (
-        x_ptr, r_ptr, _need(weight, "weight", shape[1:], torch.bfloat16, dev)), (h_ptr, n_ptr)
-
-
 def int8_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None, eps: float,
                           residual: torch.Tensor | None = None, out: tuple | None = None,
                           residual_out: torch.Tensor | None = None,
@@ -400,17 +367,14 @@ def int8_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None, eps: flo
     Returns (codes int8 [rows, K], scales fp32 [rows], h): h is residual_out, allocated when
     it is not given, or None without a residual.  residual_out may be x or residual itself.
     norm_out, when given, receives n."""
-    dev, residual_out, ins, outs = _norm_inputs(x, weight, residual, residual_out, norm_out)
-    R, K = x.shape
-    if out is None:
-        out = (torch.empty(R, K, dtype=torch.int8, device=dev),
-               torch.empty(R, dtype=torch.float32, device=dev))
-    q, s = out
-    args = (
-        *ins, eps, R, K, _need(q, "codes", x.shape, torch.int8, dev),
-        _need(s, "scales", x.shape[:1], torch.float32, dev), *outs, _stream(stream))
-    if R:   # an empty tensor has no address
-        _check("int8_rmsnorm_quantize", lib().int8_rmsnorm_quantize(*args))
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    q, s = out or (torch.empty(x.shape, dtype=torch.int8, device=x.device),
+                   torch.empty(x.shape[:1], dtype=torch.float32, device=x.device))
+    st = _calls().int8_rmsnorm_quantize(x, weight, eps, residual, q, s, residual_out, norm_out,
+                                        None if stream is None else stream.cuda_stream)
+    if st:
+        raise NVFP4Error("int8_rmsnorm_quantize", st)
     return q, s, residual_out
 
 
@@ -424,22 +388,24 @@ def nvfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None, gsf: to
 
     Returns (packed uint8 [rows, K/2], scales uint8 [scale_bytes], h).  With gsf_w and
     alpha_out the kernel also writes alpha = 1/(gsf * gsf_w)."""
-    dev, residual_out, ins, outs = _norm_inputs(x, weight, residual, residual_out, norm_out)
-    R, K = x.shape
-    one = (1,)
-    if out is None:
-        out = (torch.empty(R, K // 2, dtype=torch.uint8, device=dev),
-               torch.empty(nvfp4_scale_bytes(R, K), dtype=torch.uint8, device=dev))
-    packed, sf = out
-    args = (
-        *ins, eps, R, K, _need(gsf, "gsf", one, torch.float32, dev),
-        _need(packed, "packed", (R, K // 2), torch.uint8, dev),
-        _need_bytes(sf, "scales", lib().nvfp4_scale_bytes(R, K), dev),
-        _need(gsf_w, "gsf_w", one, torch.float32, dev),
-        _need(alpha_out, "alpha_out", one, torch.float32, dev), *outs, _stream(stream))
-    if R:   # an empty tensor has no address
-        _check("nvfp4_rmsnorm_quantize", lib().nvfp4_rmsnorm_quantize(*args))
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    calls = _calls()
+    packed, sf = out or _packed_like(x)
+    st = calls.nvfp4_rmsnorm_quantize(x, weight, eps, residual, gsf, packed, sf, gsf_w, alpha_out,
+                                      residual_out, norm_out,
+                                      None if stream is None else stream.cuda_stream)
+    if st:
+        raise NVFP4Error("nvfp4_rmsnorm_quantize", st)
     return packed, sf, residual_out
+
+
+def _packed_like(x: torch.Tensor):
+    if x.dim() != 2:
+        raise ValueError("x must be a contiguous 2-D tensor")
+    R, K = x.shape
+    return (torch.empty(R, K // 2, dtype=torch.uint8, device=x.device),
+            torch.empty(nvfp4_scale_bytes(R, K), dtype=torch.uint8, device=x.device))
 
 
 # ---------------------------------------------------------------------------
@@ -458,19 +424,15 @@ def interleave_gate_up(gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
     return torch.stack((gate, up), dim=1).reshape(2 * gate.shape[0], *gate.shape[1:])
 
 
-def _epilogue(activation, gated, residual, bias, out, M, N, dev):
-    if activation not in ACTIVATIONS:
+def _activation(activation: str, gated: bool, N: int) -> int:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
-    if gated and N % 2:
+    if not gated:
+        return act
+    if N % 2:
         raise ValueError("a gated product has an even number of weight rows")
-    shape = (M, N // 2 if gated else N)
-    y = torch.empty(shape, dtype=torch.bfloat16, device=dev) if out is None else out
-    y_ptr = _need(y, "out", shape, torch.bfloat16, dev)
-    r_ptr = _need(residual, "residual", shape, torch.bfloat16, dev)
-    if r_ptr is not None and 0 < abs(r_ptr - y_ptr) < 2 * y.numel():
-        raise ValueError("residual must be out itself or not overlap it")
-    return (y, y_ptr, r_ptr, _need(bias, "bias", (N,), torch.bfloat16, dev),
-            ACTIVATIONS[activation] + (ACT_GATED if gated else 0))
+    return act + ACT_GATED
 
 
 def nvfp4_gemm_act(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: torch.Tensor,
@@ -481,17 +443,14 @@ def nvfp4_gemm_act(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: tor
     """y bf16 = bf16(act(alpha * deq(a) deq(b)^T + bias) + residual); gated: over the column
     pairs (gate, up) of a weight in the order of interleave_gate_up, y [M, N/2].  With
     prepared=True, sfb is the output of prepare_weight_scales.  residual may be out."""
-    dev = _here(a, "a")
-    L = lib()
-    y, y_ptr, r_ptr, b_ptr, act = _epilogue(activation, gated, residual, bias, out, M, N, dev)
-    sfb_bytes = L.nvfp4_prepared_scale_bytes(N, K) if prepared else L.nvfp4_scale_bytes(N, K)
-    args = (
-        _need_bytes(a, "a", M * K // 2, dev), _need_bytes(sfa, "sfa", L.nvfp4_scale_bytes(M, K), dev),
-        _need_bytes(b, "b", N * K // 2, dev), _need_bytes(sfb, "sfb", sfb_bytes, dev),
-        1 if prepared else 0, _need(alpha, "alpha", (1,), torch.float32, dev), b_ptr, act, r_ptr,
-        y_ptr, M, N, K, _stream(stream))
-    if M and N:   # an empty tensor has no address
-        _check("nvfp4_gemm_act", L.nvfp4_gemm_act(*args))
+    act = _activation(activation, gated, N)
+    y = out
+    if y is None:
+        y = torch.empty(M, N // 2 if gated else N, dtype=torch.bfloat16, device=a.device)
+    st = _calls().nvfp4_gemm_act(a, sfa, b, sfb, prepared, alpha, bias, act, residual, y, M, N, K,
+                                 None if stream is None else stream.cuda_stream)
+    if st:
+        raise NVFP4Error("nvfp4_gemm_act", st)
     return y
 
 
@@ -501,18 +460,15 @@ def int8_gemm_act(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.
                   stream=None) -> torch.Tensor:
     """y bf16 = bf16(act((fp32(a b^T) * sa[m]) * sb[n] + bias) + residual); gated as in
     nvfp4_gemm_act.  residual may be out."""
-    dev = _here(a, "a")
-    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
-        raise ValueError("a [M, K] and b [N, K] must be 2-D with the same K")
-    M, K = a.shape
     N = b.shape[0]
-    y, y_ptr, r_ptr, b_ptr, act = _epilogue(activation, gated, residual, bias, out, M, N, dev)
-    args = (
-        _need(a, "a", a.shape, torch.int8, dev), _need(sa, "sa", (M,), torch.float32, dev),
-        _need(b, "b", b.shape, torch.int8, dev), _need(sb, "sb", (N,), torch.float32, dev),
-        b_ptr, act, r_ptr, y_ptr, M, N, K, _stream(stream))
-    if M and N:   # an empty tensor has no address
-        _check("int8_gemm_act", lib().int8_gemm_act(*args))
+    act = _activation(activation, gated, N)
+    y = out
+    if y is None:
+        y = torch.empty(a.shape[0], N // 2 if gated else N, dtype=torch.bfloat16, device=a.device)
+    st = _calls().int8_gemm_act(a, sa, b, sb, bias, act, residual, y,
+                                None if stream is None else stream.cuda_stream)
+    if st:
+        raise NVFP4Error("int8_gemm_act", st)
     return y
 
 
@@ -524,23 +480,19 @@ def nvfp4_linear_act(x: torch.Tensor, w_packed: torch.Tensor, w_sf: torch.Tensor
                      prepared: bool = False, workspace: torch.Tensor | None = None,
                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """nvfp4_linear ending in the epilogue of nvfp4_gemm_act."""
-    dev = _here(x, "x")
-    _bf16_2d(x, "x")
+    act = _activation(activation, gated, N)
     M, K = x.shape
-    L = lib()
-    y, y_ptr, r_ptr, b_ptr, act = _epilogue(activation, gated, residual, bias, out, M, N, dev)
+    y = out
+    if y is None:
+        y = torch.empty(M, N // 2 if gated else N, dtype=torch.bfloat16, device=x.device)
     if workspace is None:
-        workspace = torch.empty(nvfp4_linear_workspace_bytes(M, K), dtype=torch.uint8, device=dev)
-    ws_ptr = _need_bytes(workspace, "workspace", 0, dev)
-    sf_bytes = L.nvfp4_prepared_scale_bytes(N, K) if prepared else L.nvfp4_scale_bytes(N, K)
-    args = (
-        x.data_ptr(), M, K, _need_bytes(w_packed, "w_packed", N * K // 2, dev),
-        _need_bytes(w_sf, "w_sf", sf_bytes, dev), 1 if prepared else 0,
-        _need(gsf_w, "gsf_w", (1,), torch.float32, dev), N, b_ptr,
-        _need(gsf_x, "gsf_x", (1,), torch.float32, dev), int(rotate_group), act, r_ptr, ws_ptr,
-        workspace.numel(), y_ptr, _stream(stream))
-    if M and N:   # an empty tensor has no address
-        _check("nvfp4_linear_act", L.nvfp4_linear_act(*args))
+        workspace = torch.empty(nvfp4_linear_workspace_bytes(M, K), dtype=torch.uint8,
+                                device=x.device)
+    st = _calls().nvfp4_linear_act(x, w_packed, w_sf, prepared, gsf_w, N, bias, gsf_x,
+                                   rotate_group, act, residual, workspace, y,
+                                   None if stream is None else stream.cuda_stream)
+    if st:
+        raise NVFP4Error("nvfp4_linear_act", st)
     return y
 
 
@@ -550,22 +502,19 @@ def int8_linear_act(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
                     workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
                     stream=None) -> torch.Tensor:
     """int8_linear ending in the epilogue of int8_gemm_act."""
-    dev = _here(x, "x")
-    _bf16_2d(x, "x")
-    M, K = x.shape
     N = wq.shape[0]
-    L = lib()
-    y, y_ptr, r_ptr, b_ptr, act = _epilogue(activation, gated, residual, bias, out, M, N, dev)
+    act = _activation(activation, gated, N)
+    M, K = x.shape
+    y = out
+    if y is None:
+        y = torch.empty(M, N // 2 if gated else N, dtype=torch.bfloat16, device=x.device)
     if workspace is None:
-        workspace = torch.empty(max(int(L.int8_linear_workspace_bytes(M, K)), 1),
-                                dtype=torch.uint8, device=dev)
-    ws_ptr = _need_bytes(workspace, "workspace", 0, dev)
-    args = (
-        x.data_ptr(), M, K, _need(wq, "wq", (N, K), torch.int8, dev),
-        _need(sw, "sw", (N,), torch.float32, dev), N, b_ptr, act, r_ptr, ws_ptr,
-        workspace.numel(), y_ptr, _stream(stream))
-    if M and N:   # an empty tensor has no address
-        _check("int8_linear_act", L.int8_linear_act(*args))
+        workspace = torch.empty(max(int(lib().int8_linear_workspace_bytes(M, K)), 1),
+                                dtype=torch.uint8, device=x.device)
+    st = _calls().int8_linear_act(x, wq, sw, bias, act, residual, workspace, y,
+                                  None if stream is None else stream.cuda_stream)
+    if st:
+        raise NVFP4Error("int8_linear_act", st)
     return y
 
 

@@ -3,7 +3,9 @@
 Compiles every ``csrc/*.cu`` for sm_100a only (``-gencode
 arch=compute_100a,code=sm_100a``), one object per file in parallel under ``_build/``,
 and links them with the CUDA runtime linked statically, so the library does not
-depend on the runtime version PyTorch ships.  No GPU is needed to build.
+depend on the runtime version PyTorch ships.  ``csrc/binding.cpp``, the compiled part of the
+Python binding, becomes an extension module next to it (g++, PyTorch's headers).  No GPU is
+needed to build.
 """
 from __future__ import annotations
 
@@ -53,11 +55,39 @@ def up_to_date() -> bool:
 
 
 OBJ_DIR = os.path.join(ROOT, "_build")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The extension module of the Python binding.  It links against PyTorch only: the CUDA
+    library's entry points are handed to it by address."""
+    newest = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(INCLUDE, "nvfp4.h"), __file__))
+    if not force and os.path.exists(BINDING_PATH) and os.path.getmtime(BINDING_PATH) >= newest:
+        return BINDING_PATH
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    includes = include_paths() + [os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    tmp = BINDING_PATH + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[a for d in includes for a in ("-isystem", d)], "-o", tmp, BINDING_SRC, "-L", lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     """Each translation unit is compiled to an object in parallel (they share no device
     symbols), then nvcc links the shared object."""
+    build_binding(force, verbose)
     if not force and up_to_date():
         return LIB_PATH
     from concurrent.futures import ThreadPoolExecutor

@@ -176,3 +176,19 @@ def test_no_rows_and_other_stream():
     side.synchronize()
     for a, b, c in zip(got, want, explicit):
         assert torch.equal(a, b) and torch.equal(c, b)
+
+
+def test_refusals_with_cuda_tensors():
+    x, r, w = on(*inputs(4, 64, seed=9))
+    with pytest.raises(TypeError, match="must be on"):
+        nv.int8_rmsnorm_quantize(x, w.cpu(), EPS, residual=r)
+    with pytest.raises(nv.NVFP4Error) as e:
+        nv.int8_rmsnorm_quantize(x, w, 0.0, residual=r)
+    assert e.value.status == nv.ERR_INVALID_ARG
+    with pytest.raises(nv.NVFP4Error) as e:
+        nv.int8_rmsnorm_quantize(x[:, :24].contiguous(), w[:24], EPS)
+    assert e.value.status == nv.ERR_SHAPE
+    big = torch.zeros(4 * 64 + 1, dtype=torch.bfloat16, device=DEV)[1:].view(4, 64)
+    with pytest.raises(nv.NVFP4Error) as e:
+        nv.int8_rmsnorm_quantize(big, w, EPS)
+    assert e.value.status == nv.ERR_ALIGN

@@ -106,87 +106,107 @@ def test_product_extras(L):
     assert nvfp4_linear(L, g=48) == nv.ERR_INVALID_ARG
 
 
-def test_binding_refuses_cpu_tensors():
-    x = torch.zeros(4, 64, dtype=torch.bfloat16)
-    q = torch.zeros(4, 64, dtype=torch.int8)
-    s = torch.zeros(4)
-    u = torch.zeros(4, 32, dtype=torch.uint8)
-    for call in (lambda: nv.int8_rmsnorm_quantize(x, None, 1e-6),
-                 lambda: nv.nvfp4_rmsnorm_quantize(x, None, s[:1], 1e-6),
-                 lambda: nv.int8_gemm_act(q, s, q, s),
-                 lambda: nv.nvfp4_gemm_act(u, u, u, u, s[:1], None, 4, 4, 64),
-                 lambda: nv.int8_linear_act(x, q, s),
-                 lambda: nv.nvfp4_linear_act(x, u, u, s[:1], 4)):
-        with pytest.raises(TypeError):
-            call()
+BF16, I8, U8, F32 = torch.bfloat16, torch.int8, torch.uint8, torch.float32
 
 
-class FakeTensor:
-    """What the binding's checks read of a tensor, at a made-up address."""
-    is_cuda = True
-
-    def __init__(self, shape, dtype, ptr, device="cuda:0", contiguous=True):
-        self.shape, self.dtype, self.ptr = torch.Size(shape), dtype, ptr
-        self.device, self.c = torch.device(device), contiguous
-
-    def is_contiguous(self):
-        return self.c
-
-    def data_ptr(self):
-        return self.ptr
-
-    def dim(self):
-        return len(self.shape)
-
-    def numel(self):
-        return self.shape.numel()
-
-    def element_size(self):
-        return torch.empty(0, dtype=self.dtype).element_size()
+def z(*shape, dtype=BF16):
+    return torch.zeros(*shape, dtype=dtype)
 
 
-BF16 = torch.bfloat16
+def norms():
+    """The two norms as one call each of keyword arguments, with arguments that only a CPU
+    tensor makes wrong (the device is checked last)."""
+    base = dict(x=z(4, 64), weight=z(64), eps=1e-6, residual=z(4, 64), residual_out=z(4, 64))
+    return [(nv.int8_rmsnorm_quantize, dict(base, out=(z(4, 64, dtype=I8), z(4, dtype=F32)))),
+            (nv.nvfp4_rmsnorm_quantize,
+             dict(base, gsf=z(1, dtype=F32), out=(z(4, 32, dtype=U8), z(512, dtype=U8))))]
 
 
-def test_argument_checks(monkeypatch):
-    dev = torch.device("cuda:0")
-    t = FakeTensor((4, 64), BF16, 4096)
-    assert nv._need(t, "t", (4, 64), BF16, dev) == 4096
-    assert nv._need(None, "t", (4, 64), BF16, dev) is None
-    for bad in (FakeTensor((4, 64), torch.float16, 0), FakeTensor((4, 64), BF16, 0, "cuda:1")):
-        with pytest.raises(TypeError):
-            nv._need(bad, "t", (4, 64), BF16, dev)
-    for bad in (FakeTensor((4, 63), BF16, 0), FakeTensor((4, 64), BF16, 0, contiguous=False)):
-        with pytest.raises(ValueError):
-            nv._need(bad, "t", (4, 64), BF16, dev)
-    with pytest.raises(ValueError):
-        nv._need_bytes(FakeTensor((15,), torch.uint8, 0), "t", 16, dev)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    with pytest.raises(ValueError, match="current device"):
-        nv._here(t, "t")
+def products():
+    a, b = z(4, 64, dtype=I8), z(8, 64, dtype=I8)
+    p, q, sf = z(4, 32, dtype=U8), z(8, 32, dtype=U8), z(512, dtype=U8)
+    one = z(1, dtype=F32)
+    base = dict(bias=z(8), activation="silu", residual=z(4, 8), out=z(4, 8))
+    ws = z(1 << 16, dtype=U8)
+    return [(nv.int8_gemm_act, dict(base, a=a, sa=z(4, dtype=F32), b=b, sb=z(8, dtype=F32))),
+            (nv.nvfp4_gemm_act, dict(base, a=p, sfa=sf, b=q, sfb=sf, alpha=one, M=4, N=8, K=64)),
+            (nv.int8_linear_act, dict(base, x=z(4, 64), wq=b, sw=z(8, dtype=F32), workspace=ws)),
+            (nv.nvfp4_linear_act, dict(base, x=z(4, 64), w_packed=q, w_sf=sf, gsf_w=one, N=8,
+                                       workspace=ws))]
 
 
-def test_overlaps_are_refused(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    x = FakeTensor((4, 64), BF16, 4096)
-    r = FakeTensor((4, 64), BF16, 8192)
-    half = FakeTensor((4, 64), BF16, 4096 + 256)
-    with pytest.raises(ValueError, match="residual_out"):
-        nv._norm_inputs(x, None, r, half, None)
-    with pytest.raises(ValueError, match="residual_out"):
-        nv._norm_inputs(x, None, None, r, None)
-    with pytest.raises(ValueError, match="norm_out"):
-        nv._norm_inputs(x, None, r, r, x)
-    nv._norm_inputs(x, None, r, r, None)                   # in place is fine
-    y = FakeTensor((4, 8), BF16, 4096)
-    near = FakeTensor((4, 8), BF16, 4096 + 16)
-    with pytest.raises(ValueError, match="residual"):
-        nv._epilogue("silu", False, near, None, y, 4, 8, x.device)
-    nv._epilogue("silu", False, y, None, y, 4, 8, x.device)
-    with pytest.raises(ValueError, match="even"):
-        nv._epilogue("silu", True, None, None, None, 4, 9, x.device)
-    with pytest.raises(ValueError, match="activation"):
-        nv._epilogue("swish", False, None, None, y, 4, 8, x.device)
+def refuses(f, kw, error, match, **change):
+    with pytest.raises(error, match=match):
+        f(**dict(kw, **change))
+
+
+def test_norm_tensors():
+    for f, kw in norms():
+        refuses(f, kw, TypeError, "CUDA")                     # all else is right
+        refuses(f, kw, TypeError, "x must be a BFloat16", x=z(4, 64, dtype=torch.float16))
+        refuses(f, kw, ValueError, "2-D", x=z(64))
+        refuses(f, kw, ValueError, "contiguous", x=z(4, 128)[:, ::2])
+        refuses(f, kw, ValueError, "residual must be", residual=z(4, 32))
+        refuses(f, kw, TypeError, "residual must be", residual=z(4, 64, dtype=F32))
+        refuses(f, kw, ValueError, "weight must be", weight=z(65))
+        refuses(f, kw, ValueError, "residual_out must be", residual_out=z(5, 64))
+        refuses(f, kw, ValueError, "needs a residual", residual=None)
+        refuses(f, kw, ValueError, "norm_out must be", norm_out=z(4, 63))
+        refuses(f, kw, TypeError, "weight must be on", weight=z(64).to("meta"))
+        refuses(f, kw, TypeError, "eps", eps="small")
+        both = z(8, 64)
+        refuses(f, kw, ValueError, "residual_out must be x or residual", x=both[:4], residual_out=both[2:6])
+        refuses(f, kw, ValueError, "norm_out must not overlap", x=both[:4], norm_out=both[:4])
+        refuses(f, kw, ValueError, "norm_out must not overlap", residual_out=both[:4], norm_out=both[3:7])
+        refuses(f, kw, TypeError, "CUDA", residual_out=kw["x"])        # in place is right
+        refuses(f, kw, TypeError, "CUDA", residual_out=kw["residual"])
+        line = z(5, 64)
+        refuses(f, kw, ValueError, "weight must not overlap", weight=line[4], residual_out=line[1:])
+    (f8, k8), (f4, k4) = norms()
+    refuses(f8, k8, ValueError, "codes", out=(z(4, 63, dtype=I8), z(4, dtype=F32)))
+    refuses(f8, k8, ValueError, "scales", out=(z(4, 64, dtype=I8), z(5, dtype=F32)))
+    refuses(f4, k4, ValueError, "packed", out=(z(4, 64, dtype=U8), z(512, dtype=U8)))
+    refuses(f4, k4, ValueError, "scales", out=(z(4, 32, dtype=U8), z(511, dtype=U8)))
+    refuses(f4, k4, ValueError, "gsf must be", gsf=z(2, dtype=F32))
+    refuses(f4, k4, TypeError, "gsf must be a tensor", gsf=1.0)
+    refuses(f4, k4, TypeError, "alpha_out", alpha_out=z(1))
+
+
+def test_product_tensors():
+    for f, kw in products():
+        refuses(f, kw, TypeError, "CUDA")
+        refuses(f, kw, ValueError, "activation", activation="swish")
+        refuses(f, kw, ValueError, "bias must be", bias=z(9))
+        refuses(f, kw, TypeError, "bias must be", bias=z(8, dtype=F32))
+        refuses(f, kw, ValueError, "out must be", out=z(4, 7))
+        refuses(f, kw, ValueError, "out must be", gated=True)          # needs N / 2 columns
+        refuses(f, kw, ValueError, "residual must be", residual=z(4, 16)[:, ::2])
+        refuses(f, kw, TypeError, "residual must be on", residual=z(4, 8).to("meta"))
+        both = z(8, 8)
+        refuses(f, kw, ValueError, "residual must be out", residual=both[:4], out=both[1:5])
+        refuses(f, kw, TypeError, "CUDA", residual=kw["out"])          # in place is right
+        refuses(f, kw, TypeError, "CUDA", gated=True, out=z(4, 4), residual=None)
+    (g8, a8), (g4, a4), (l8, b8), (l4, b4) = products()
+    refuses(g8, a8, ValueError, "even", gated=True, b=z(9, 64, dtype=I8))
+    refuses(g8, a8, ValueError, "b must be", b=z(8, 32, dtype=I8))
+    refuses(g8, a8, ValueError, "sa must be", sa=z(5, dtype=F32))
+    refuses(g8, a8, TypeError, "a must be", a=z(4, 64, dtype=U8))
+    refuses(g4, a4, ValueError, "a must be", a=z(4, 31, dtype=U8))
+    refuses(g4, a4, ValueError, "sfb must be", sfb=z(511, dtype=U8))
+    refuses(g4, a4, ValueError, "sfb must be", prepared=True)          # prepared blocks are longer
+    refuses(g4, a4, ValueError, "alpha must be", alpha=z(2, dtype=F32))
+    refuses(l8, b8, TypeError, "workspace", workspace=z(64))
+    refuses(l4, b4, ValueError, "w_packed", w_packed=z(8, 31, dtype=U8))
+    refuses(l4, b4, ValueError, "gsf_x must be", gsf_x=z(0, dtype=F32))
+
+
+def test_extension_module():
+    calls = nv._calls()
+    assert all(hasattr(calls, n) for n in nv._BOUND[:6])
+    with pytest.raises(TypeError):
+        calls.int8_rmsnorm_quantize(1, 2)                              # wrong number of arguments
+    with pytest.raises(TypeError, match="x must be a tensor"):
+        calls.int8_rmsnorm_quantize(*([None] * 9))
 
 
 def test_interleave_gate_up():
