@@ -14,8 +14,13 @@
 //
 // Layout: a unit is 16 consecutive values of a row (one NVFP4 block; 32 bytes of bf16, 16
 // of int8 codes).  A thread owns C units of a row, lane-contiguous, so a row is read once
-// into registers and every store is 16 bytes wide (8 for FP4 codes).  Rows of up to 2048
-// values take one warp each (no block barrier); longer ones one block each.
+// into registers and every store is 16 bytes wide (8 for FP4 codes).
+//
+// Bound by HBM: with a residual 7 bytes a value (int8; 6.56 FP4), each moved once.  B200,
+// graph replay: 32768 x 5120 int8 215 us, 5.47 TB/s (0.84 of the measured copy rate);
+// 32768 x 1024 FP4 37.8 us, 5.83 TB/s (0.89); a single row of 5120 3.0 us, of which a launch
+// alone takes two.  Fetching the next row while the current one is worked on gained nothing
+// (225 us): six blocks of 320 threads on an SM cover the latency already.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -262,10 +267,13 @@ nvfp4_status launch_norm(const NormParams& p, int threads, const DeviceInfo& dev
 
 template <bool FP4>
 nvfp4_status dispatch_norm(const NormParams& p, const DeviceInfo& dev, cudaStream_t stream) {
+    // A warp per row as long as a lane has one unit (no block barrier; 32768 x 512 int8 22.5
+    // us against 26.3 with a block per row), then a block per row with one unit per thread:
+    // more units on fewer threads lengthen the chain of a row (1040 values, int8: 777 rows
+    // 5.7 us with a warp of three units a lane, 3.5 with a block of 96 threads; 32768 rows
+    // 89.6 and 65.0).  Above 1024 units a thread takes two or four.
     const int U = p.units_padded;
     if (U <= 32) return launch_norm<FP4, 1, false>(p, kNormWarpThreads, dev, stream);
-    if (U <= 64) return launch_norm<FP4, 2, false>(p, kNormWarpThreads, dev, stream);
-    if (U <= 128) return launch_norm<FP4, 4, false>(p, kNormWarpThreads, dev, stream);
     if (U <= 1024) return launch_norm<FP4, 1, true>(p, (U + 31) / 32 * 32, dev, stream);
     if (U <= 2048) return launch_norm<FP4, 2, true>(p, ((U + 1) / 2 + 31) / 32 * 32, dev, stream);
     return launch_norm<FP4, 4, true>(p, ((U + 3) / 4 + 31) / 32 * 32, dev, stream);

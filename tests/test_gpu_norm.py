@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda"
 EPS = 1e-6
 SHAPES = [(1, 16), (1, 5120), (3, 48), (37, 80), (129, 512), (5, 528), (64, 1024), (7, 1040),
-          (33, 2048), (9, 2064), (300, 5120), (2, 16384), (3, 16400), (2, 25600), (1, 32784),
+          (33, 2048), (9, 2064), (300, 5120), (700, 496), (6, 544), (2, 16384), (3, 16400), (2, 25600), (1, 32784),
           (2, 65536)]
 
 
