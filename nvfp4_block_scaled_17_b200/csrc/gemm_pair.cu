@@ -788,8 +788,15 @@ nvfp4_status launch_gemm_act(const GemmActArgs& g, cudaStream_t stream) {
     DeviceInfo dev;
     nvfp4_status st = device_info(&dev);
     if (st != NVFP4_OK) return st;
-    const bool long_weight = (g.N + 255) / 256 * 2 > dev.sms;   // no cluster left to split K over
-    if (g.M <= kStreamMaxRows && long_weight) return launch_gemm_stream(g, stream);
+    // A weight whose 256-row tiles leave no SMs to split K over streams through all SMs for up
+    // to 32 rows, and for up to 64 when K is long enough (20 stages) to cover the stream
+    // kernel's narrow stores.  Against SM pairs, us: 51200 x 5120 FP4 at 1 row 31 : 42, 64 rows
+    // 37 : 42, 128 rows 48 : 43; 20480 x 2560 FP4 (10 stages) 32 rows 14.5 : 17.7, 64 rows
+    // 18.7 : 17.3; 19456 x 512 int8 32 rows 9.3 : 10.9, 48 rows 12.3 : 11.0.
+    const bool long_weight = (g.N + 255) / 256 * 2 > dev.sms;
+    const int64_t stages = ((g.int8 ? g.K : g.K / 2) + 127) / 128;
+    if (long_weight && (g.M <= kSmallMaxRows || (g.M <= kStreamMaxRows && stages >= 20)))
+        return launch_gemm_stream(g, stream);
     if (g.M <= kSmallMaxRows) return launch_gemm_small_act(g, stream);
     bool taken = false;
     st = launch_gemm_act_split_k(g, &taken, stream);

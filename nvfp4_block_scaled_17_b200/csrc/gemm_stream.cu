@@ -1,7 +1,7 @@
 // gemm_stream.cu -- the products with an activation and a residual in their epilogue, for few
 // activation rows and a weight that is long enough to occupy every SM.
 //
-// With M <= 128 rows the call is the weight's one trip from HBM (N x K bytes, or 9/16 of them
+// With M <= 64 rows the call is the weight's one trip from HBM (N x K bytes, or 9/16 of them
 // for FP4), so the design keeps that stream going: one persistent CTA per SM walks tiles of
 // 128 weight rows, and its copies run ahead across tile boundaries, as many stages as shared
 // memory holds (nine of 22 KiB at M = 16).  The operands are swapped as in gemm_small.cu: the
@@ -35,9 +35,10 @@ constexpr int TS_W = TROWS * TKB;             // 16 KiB
 constexpr int TS_SF = 4 * 512;                // one operand's scale chunks of a stage
 constexpr int TSMEM = 232448;                 // all that a CTA can have
 constexpr int TS_BARRIERS = 512;
-constexpr uint32_t TTMEM_ACC1 = 128;
-constexpr uint32_t TTMEM_SF = 256;            // scale ring: slots of 4 columns each for W and x
+constexpr uint32_t TTMEM_ACC1 = 64;           // second accumulator (kStreamMaxRows columns each)
+constexpr uint32_t TTMEM_SF = 128;            // scale ring: slots of 4 columns each for W and x
 constexpr int TSF_SLOTS = 5;
+constexpr int TTMEM_COLS = 256;
 
 struct StreamParams {
     const uint8_t* sfw;        // weight scales: 128x4, or prepared
@@ -115,7 +116,7 @@ gemm_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 1) tmem_alloc(tmem_holder, 512);
+    if (warp == 1) tmem_alloc(tmem_holder, TTMEM_COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -294,7 +295,7 @@ gemm_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, TTMEM_COLS);
     }
 }
 

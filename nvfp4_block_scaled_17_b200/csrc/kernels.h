@@ -134,11 +134,12 @@ struct GemmActArgs {
     bool weights_ready;        // as in launch_gemm
 };
 
-// Picks the schedule (gemm_pair.cu): the swapped-operand kernel for few rows, split-K for
-// grids of few tiles (taken says whether it was launched), SM pairs for the rest.
+// Picks the schedule (gemm_pair.cu): for few rows the swapped-operand kernels, a streaming one
+// for long weights and one of clusters; split-K for grids of few tiles (taken says whether it
+// was launched); SM pairs for the rest.
 nvfp4_status launch_gemm_act(const GemmActArgs& g, cudaStream_t stream);
 nvfp4_status launch_gemm_small_act(const GemmActArgs& g, cudaStream_t stream);
-constexpr int64_t kStreamMaxRows = 128;
+constexpr int64_t kStreamMaxRows = 64;
 nvfp4_status launch_gemm_stream(const GemmActArgs& g, cudaStream_t stream);
 nvfp4_status launch_gemm_act_split_k(const GemmActArgs& g, bool* taken, cudaStream_t stream);
 

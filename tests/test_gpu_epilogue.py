@@ -281,8 +281,8 @@ def test_block_in_a_graph(kind, M):
 
 
 @pytest.mark.parametrize("kind", ["int8", "nvfp4"])
-@pytest.mark.parametrize("M", [1, 16, 17, 128])
-@pytest.mark.parametrize("N,K", [(19200, 320), (38038, 64), (25602, 1152)])
+@pytest.mark.parametrize("M", [1, 16, 17, 32, 64, 128])
+@pytest.mark.parametrize("N,K", [(19200, 320), (38038, 64), (25602, 1152), (19202, 5184)])
 def test_long_weights(kind, M, N, K):
     """Few rows against a weight with more row blocks than SMs."""
     one(kind, M, N, K, "silu", True, True, True, prepared=True)
@@ -327,3 +327,41 @@ def test_split_k(kind, M, N, K, gated):
     """Few tiles of a long K: clusters that share it."""
     one(kind, M, N, K, "silu", gated, True, True, prepared=True)
     one(kind, M, N, K, "gelu", gated, False, False)
+
+
+@pytest.mark.parametrize("kind", ["int8", "nvfp4"])
+def test_two_streams_at_once(kind):
+    """Calls of every schedule on two streams, none waiting for the other."""
+    shapes = [(1, 19456, 512), (4, 1024, 2048), (100, 520, 2048), (2500, 1024, 512)]
+    jobs = []
+    for M, N, K in shapes:
+        ops = operands(kind, M, N, K)
+        b, r = extras(M, N, False, True, True)
+        want = run(kind, ops, M, N, K, b, "silu", False, r)
+        outs = [torch.empty_like(want) for _ in range(2)]
+        jobs.append((ops, M, N, K, b, r, want, outs))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for ops, M, N, K, b, r, _, outs in jobs:
+            for s, out in zip(streams, outs):
+                run(kind, ops, M, N, K, b, "silu", False, r, out=out, stream=s)
+    torch.cuda.synchronize()
+    assert nv.last_device_status() == nv.OK
+    for *_, want, outs in jobs:
+        for out in outs:
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+def test_refusals_with_cuda_tensors():
+    ops = operands("int8", 4, 16, 64)
+    with pytest.raises(TypeError, match="must be on"):
+        nv.int8_gemm_act(ops[0], ops[1].cpu(), ops[2], ops[3])
+    y = torch.empty(4 * 16 + 1, dtype=BF16, device=DEV)[1:].view(4, 16)
+    with pytest.raises(nv.NVFP4Error) as e:
+        nv.int8_gemm_act(ops[0], ops[1], ops[2], ops[3], out=y)
+    assert e.value.status == nv.ERR_ALIGN
+    with pytest.raises(nv.NVFP4Error) as e:
+        nv.int8_linear_act(torch.zeros(4, 64, dtype=BF16, device=DEV), ops[2], ops[3],
+                           workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
+    assert e.value.status == nv.ERR_WORKSPACE
