@@ -26,7 +26,7 @@
 // The tiles of a last, at most half full wave are cut into two of 128 columns each, which
 // then all run at once: 4096 x 5120 x 25600 is 320 tiles on 74 pairs, 4.5 waves instead of 5.
 // int8 accumulators are two full 256-column buffers; FP4 ones share 64 columns ([0, 256) and
-// [192, 448)) to leave room for the scale ring at [448, 508).
+// [192, 448)) to leave room for the scales of a stage's four K steps at [448, 496).
 //
 // Every wait is bounded; on expiry the kernel records NVFP4_ERR_TIMEOUT, lets its copies
 // land, frees tensor memory and returns.  No load uses cluster multicast.
@@ -61,7 +61,6 @@ struct PairSmem {
 static_assert(PairSmem<false>::BYTES <= 232448 && PairSmem<true>::BYTES <= 232448,
               "dynamic shared memory above the 227 KiB a CTA can have");
 constexpr uint32_t PTMEM_SF = 448;
-constexpr int PSF_SLOTS = 5;
 // E2M1 x E2M1 (format 1), or signed int8 (format 1) with an int32 accumulator; K-major,
 // N = 256, M = 256 over the pair
 constexpr uint32_t PIDESC = (1u << 7) | (1u << 10) | ((uint32_t)(PN >> 3) << 17) | (16u << 24);
@@ -354,7 +353,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
     } else if (warp == 1) {
         if (rank == 0) {
-            int stage = 0, it = 0, sf_slot = 0;
+            int stage = 0, it = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int item = pair; ok && item < p.items; item += pairs, ++it) {
@@ -368,8 +367,11 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 }
                 tc_fence_after();
                 const uint32_t acc = tmem + (b ? (I8 ? 256u : 192u) : 0u);
-                // One loop for each width: a choice inside it costs the issue of every MMA (8192^3
-                // FP4 245 us, 306 with a branch per K step).
+                // One loop for each width, and in it a stage of four K steps without a branch, an
+                // index or a flag that the compiler does not know: whatever comes between two
+                // steps is time the tensor pipe waits.  With a test of the step against the end
+                // of K before each, and the scale slot taken from a ring, a 128-cycle step took
+                // 204 in a loop of nothing else (134 as it is), and 8192^3 FP4 234 us.
                 auto mainloop = [&](auto width) {
                     constexpr bool HALF = decltype(width)::value;
                     for (int kt = 0; kt < p.k_tiles; ++kt) {
@@ -378,24 +380,27 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                             break;
                         }
                         tc_fence_after();
-                        const int steps = min(4, p.kchunks - 4 * kt);
                         const uint32_t s = smem_u32(smem + stage * SM::STAGE);
                         const uint64_t ad = sdesc_kmajor_sw128(s), bd = sdesc_kmajor_sw128(s + PS_OP);
                         const uint64_t sad = sdesc_sf(s + 2 * PS_OP);
                         const uint64_t sbd = sdesc_sf(s + 2 * PS_OP + PS_SFA);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            if (kk < steps) {
-                                const uint32_t accumulate = (kt > 0 || kk > 0) ? 1u : 0u;
-                                if constexpr (I8) {
-                                    pair_step_i8_w<HALF>(acc, ad + 2 * kk, bd + 2 * kk, accumulate);
-                                } else {
-                                    pair_step_fp4_w<HALF>(acc, ad + 2 * kk, bd + 2 * kk,
-                                                          tmem + PTMEM_SF + 12u * (uint32_t)sf_slot,
-                                                          sad + 32 * kk, sbd + 32 * kk, accumulate);
-                                    sf_slot = sf_slot == PSF_SLOTS - 1 ? 0 : sf_slot + 1;
-                                }
-                            }
+                        auto step = [&](int kk, uint32_t accumulate) {
+                            if constexpr (I8)
+                                pair_step_i8_w<HALF>(acc, ad + 2 * kk, bd + 2 * kk, accumulate);
+                            else
+                                pair_step_fp4_w<HALF>(acc, ad + 2 * kk, bd + 2 * kk,
+                                                      tmem + PTMEM_SF + 12u * (uint32_t)kk, sad + 32 * kk,
+                                                      sbd + 32 * kk, accumulate);
+                        };
+                        const int steps = p.kchunks - 4 * kt;
+                        step(0, kt > 0 ? 1u : 0u);
+                        if (steps >= 4) {
+                            step(1, 1u);
+                            step(2, 1u);
+                            step(3, 1u);
+                        } else {                 // the end of K
+                            if (steps > 1) step(1, 1u);
+                            if (steps > 2) step(2, 1u);
                         }
                         commit_both_w(&empty[stage]);
                         if (++stage == PSTAGES) {
