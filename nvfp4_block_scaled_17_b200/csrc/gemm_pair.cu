@@ -367,11 +367,13 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 }
                 tc_fence_after();
                 const uint32_t acc = tmem + (b ? (I8 ? 256u : 192u) : 0u);
-                // One loop for each width, and in it a stage of four K steps without a branch, an
-                // index or a flag that the compiler does not know: whatever comes between two
-                // steps is time the tensor pipe waits.  With a test of the step against the end
-                // of K before each, and the scale slot taken from a ring, a 128-cycle step took
-                // 204 in a loop of nothing else (134 as it is), and 8192^3 FP4 234 us.
+                // One loop for each width, and in it four K steps to every stage, without a branch
+                // or a running index: whatever comes between two steps is time the tensor pipe
+                // waits.  In a loop of nothing else a 128-cycle step took 204 with a test against
+                // the end of K before each step and the scale slot taken from a ring, 169 with a
+                // second path for the last stage, and 134 like this.  Past the end of K both
+                // operands are zero (TMA's fill); their scales there are the next row tile's or
+                // zero, so the steps add nothing.
                 auto mainloop = [&](auto width) {
                     constexpr bool HALF = decltype(width)::value;
                     for (int kt = 0; kt < p.k_tiles; ++kt) {
@@ -392,16 +394,10 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                                                       tmem + PTMEM_SF + 12u * (uint32_t)kk, sad + 32 * kk,
                                                       sbd + 32 * kk, accumulate);
                         };
-                        const int steps = p.kchunks - 4 * kt;
                         step(0, kt > 0 ? 1u : 0u);
-                        if (steps >= 4) {
-                            step(1, 1u);
-                            step(2, 1u);
-                            step(3, 1u);
-                        } else {                 // the end of K
-                            if (steps > 1) step(1, 1u);
-                            if (steps > 2) step(2, 1u);
-                        }
+                        step(1, 1u);
+                        step(2, 1u);
+                        step(3, 1u);
                         commit_both_w(&empty[stage]);
                         if (++stage == PSTAGES) {
                             stage = 0;
