@@ -50,14 +50,13 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 template <int ACT>
 __device__ __forceinline__ float2 minus_logit2(float2 v) {
     if constexpr (ACT == NVFP4_ACT_SILU) return __fmul2_rn(v, both(-kLog2e));
-    float2 u = __fmul2_rn(v, v);
+    const float2 u = __fmul2_rn(v, v);
     if constexpr (ACT == NVFP4_ACT_GELU_TANH) {
         constexpr float c = -2.0f * 0.79788456080286535588f * kLog2e;
         return __fmul2_rn(v, __ffma2_rn(u, both(c * 0.044715f), both(c)));
     }
     // gelu: logit Phi(v) = v Q(v^2); Q fitted on |v| <= 6 for the least largest error of
-    // v Phi(v), and held at its value there beyond
-    u = make_float2(fminf(u.x, 36.0f), fminf(u.y, 36.0f));
+    // v Phi(v).  Above 6, where Phi is 1, it keeps growing (Q > 4 from there on).
     float2 q = __ffma2_rn(u, both(-kLog2e * 3.6392367769551445e-09f), both(-kLog2e * -2.680700010037935e-07f));
     q = __ffma2_rn(u, q, both(-kLog2e * 7.956275638921296e-06f));
     q = __ffma2_rn(u, q, both(-kLog2e * -0.00011060688607769335f));
@@ -71,11 +70,11 @@ template <int ACT>
 __device__ __forceinline__ float2 act_value2(float2 v) {
     if constexpr (ACT == NVFP4_ACT_NONE) return v;
     if constexpr (ACT == NVFP4_ACT_RELU) return make_float2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f));
-    const float2 t = minus_logit2<ACT>(v);
-    // exponents below 60 keep the product of two sums below 2^122; at 60 the quotient is
-    // v 2^-60, far below every bf16 next to which it could count
-    const float2 d = __fadd2_rn(
-        make_float2(ex2_approx(fminf(t.x, 60.0f)), ex2_approx(fminf(t.y, 60.0f))), both(1.0f));
+    // The logistic factor is held at its value at lo, which is below 1e-9 (silu 1e-17), so
+    // that the exponents stay below 60 and the product of two sums below 2^122.
+    constexpr float lo = ACT == NVFP4_ACT_SILU ? -40.0f : -6.0f;
+    const float2 t = minus_logit2<ACT>(make_float2(fmaxf(v.x, lo), fmaxf(v.y, lo)));
+    const float2 d = __fadd2_rn(make_float2(ex2_approx(t.x), ex2_approx(t.y)), both(1.0f));
     const float r = rcp_approx(d.x * d.y);
     return __fmul2_rn(v, __fmul2_rn(both(r), make_float2(d.y, d.x)));
 }

@@ -17,10 +17,11 @@
 // into registers and every store is 16 bytes wide (8 for FP4 codes).
 //
 // Bound by HBM: with a residual 7 bytes a value (int8; 6.56 FP4), each moved once.  B200,
-// graph replay: 32768 x 5120 int8 215 us, 5.47 TB/s (0.84 of the measured copy rate);
-// 32768 x 1024 FP4 37.8 us, 5.83 TB/s (0.89); a single row of 5120 3.0 us, of which a launch
-// alone takes two.  Fetching the next row while the current one is worked on gained nothing
-// (225 us): six blocks of 320 threads on an SM cover the latency already.
+// graph replay: 32768 x 5120 int8 196 us, 6.00 TB/s (0.92 of the measured copy rate; 215
+// before the arithmetic was packed in pairs and the codes were rounded by an addition);
+// 32768 x 1024 FP4 37.5 us, 5.87 TB/s (0.90); a single row of 5120 2.7 us, of which a launch
+// alone takes two.  Fetching the next row while the current one is worked on gained nothing:
+// six blocks of 320 threads on an SM cover the latency already.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -75,28 +76,32 @@ __device__ __forceinline__ uint32_t unit_absmax(const Unit& u) {
                         absmax2_bf16(absmax2_bf16(u.w[4], u.w[5]), absmax2_bf16(u.w[6], u.w[7])));
 }
 
+__device__ __forceinline__ float2 pair_of(uint32_t w) { return make_float2(bf16lo(w), bf16hi(w)); }
+__device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
+
 // 16 int8 codes of a unit under the row scale s; r = rn(1 / s).  rn(n / s) by one
 // remainder step (Markstein), as int8_quantize_rows computes it; a subnormal s, whose
-// reciprocal would overflow, takes the division, and s = 0 gives zeros.
+// reciprocal would overflow, takes the division, and s = 0 gives zeros.  Adding 1.5 * 2^23
+// rounds |t| <= 127 to a whole number, half to even, whose low byte is the code.
 __device__ __forceinline__ uint4 int8_codes(const Unit& u, float s, float r, bool fast) {
     uint32_t out[4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-        int c[4];
+        float2 c[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t word = u.w[2 * g + (j >> 1)];
-            const float v = (j & 1) ? bf16hi(word) : bf16lo(word);
-            float t;
+        for (int j = 0; j < 2; ++j) {
+            const float2 v = pair_of(u.w[2 * g + j]);
+            float2 t;
             if (fast) {
-                const float q0 = __fmul_rn(v, r);
-                t = __fmaf_rn(__fmaf_rn(-q0, s, v), r, q0);
+                const float2 q0 = __fmul2_rn(v, twice(r));
+                t = __ffma2_rn(__ffma2_rn(q0, twice(-s), v), twice(r), q0);
             } else {
-                t = s != 0.0f ? __fdiv_rn(v, s) : 0.0f;
+                t = s != 0.0f ? make_float2(__fdiv_rn(v.x, s), __fdiv_rn(v.y, s)) : twice(0.0f);
             }
-            c[j] = __float2int_rn(t);
+            c[j] = make_float2(__fadd_rn(t.x, 12582912.0f), __fadd_rn(t.y, 12582912.0f));
         }
-        out[g] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        out[g] = __byte_perm(__byte_perm(__float_as_uint(c[0].x), __float_as_uint(c[0].y), 0x0040),
+                             __byte_perm(__float_as_uint(c[1].x), __float_as_uint(c[1].y), 0x0040), 0x5410);
     }
     return make_uint4(out[0], out[1], out[2], out[3]);
 }
@@ -108,8 +113,9 @@ __device__ __forceinline__ uint32_t fp4_codes(const Unit& u, float gsf, uint2& c
     float v[2][8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        v[j >> 2][2 * (j & 3)] = __fmul_rn(bf16lo(u.w[j]), inv);
-        v[j >> 2][2 * (j & 3) + 1] = __fmul_rn(bf16hi(u.w[j]), inv);
+        const float2 t = __fmul2_rn(pair_of(u.w[j]), twice(inv));
+        v[j >> 2][2 * (j & 3)] = t.x;
+        v[j >> 2][2 * (j & 3) + 1] = t.y;
     }
     codes.x = s8 ? e2m1x8_from_f32(v[0]) : 0u;
     codes.y = s8 ? e2m1x8_from_f32(v[1]) : 0u;
@@ -161,9 +167,10 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : kNormWarpThreads) norm_kernel(c
                 const int64_t at = row * p.K + 16 * (int64_t)u;
                 const Unit r = load_unit(p.residual + at);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    h[i].w[j] = bf16x2_rn(__fadd_rn(bf16lo(h[i].w[j]), bf16lo(r.w[j])),
-                                          __fadd_rn(bf16hi(h[i].w[j]), bf16hi(r.w[j])));
+                for (int j = 0; j < 8; ++j) {
+                    const float2 t = __fadd2_rn(pair_of(h[i].w[j]), pair_of(r.w[j]));
+                    h[i].w[j] = bf16x2_rn(t.x, t.y);
+                }
                 if (p.h_out) store_unit(p.h_out + at, h[i]);
             }
         }
@@ -195,9 +202,10 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : kNormWarpThreads) norm_kernel(c
                     0x3f803f80u, 0x3f803f80u}};
             if (p.weight && u < p.units) w = load_unit(p.weight + 16 * (int64_t)u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                h[i].w[j] = bf16x2_rn(__fmul_rn(__fmul_rn(bf16lo(h[i].w[j]), rstd), bf16lo(w.w[j])),
-                                      __fmul_rn(__fmul_rn(bf16hi(h[i].w[j]), rstd), bf16hi(w.w[j])));
+            for (int j = 0; j < 8; ++j) {
+                const float2 t = __fmul2_rn(__fmul2_rn(pair_of(h[i].w[j]), twice(rstd)), pair_of(w.w[j]));
+                h[i].w[j] = bf16x2_rn(t.x, t.y);
+            }
             if (p.n_out && u < p.units) store_unit(p.n_out + row * p.K + 16 * (int64_t)u, h[i]);
             if constexpr (!FP4) m = absmax2_bf16(m, unit_absmax(h[i]));
         }
