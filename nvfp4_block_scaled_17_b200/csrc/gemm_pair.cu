@@ -667,6 +667,8 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
 }
 
+}  // namespace
+
 // 512-byte scale chunks as the rows of a 2-D tensor of 32-bit words, four rows per load.
 bool make_scale_map(CUtensorMap* map, const void* base, int64_t chunks) {
     auto enc = tensor_map_encoder();
@@ -679,6 +681,8 @@ bool make_scale_map(CUtensorMap* map, const void* base, int64_t chunks) {
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 using PairKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
                             CUtensorMap, CUtensorMap, PairParams);

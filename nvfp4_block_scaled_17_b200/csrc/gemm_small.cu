@@ -296,7 +296,8 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                     break;
                 }
                 tc_fence_after();
-                const int steps = min(4, p.kchunks - 4 * kt);
+                // (int8: four steps always; past the end of K both operands are zero)
+                const int steps = I8 ? 4 : min(4, p.kchunks - 4 * kt);
                 // the stage's descriptors; step kk adds 32 bytes to W and x (2 units) and
                 // 512 to the scale chunks (32 units).  Both weight scale layouts leave the
                 // stage's chunks in the same shared-memory order.

@@ -36,13 +36,10 @@ constexpr int TS_SF = 4 * 512;                // one operand's scale chunks of a
 constexpr int TSMEM = 232448;                 // all that a CTA can have
 constexpr int TS_BARRIERS = 512;
 constexpr uint32_t TTMEM_ACC1 = 64;           // second accumulator (kStreamMaxRows columns each)
-constexpr uint32_t TTMEM_SF = 128;            // scale ring: slots of 4 columns each for W and x
-constexpr int TSF_SLOTS = 5;
+constexpr uint32_t TTMEM_SF = 128;            // per K step of a stage 4 columns each for W and x
 constexpr int TTMEM_COLS = 256;
 
 struct StreamParams {
-    const uint8_t* sfw;        // weight scales: 128x4, or prepared
-    const uint8_t* sfx;        // activation 128x4 scales
     const float* alpha;
     const float* sx;           // int8: fp32 row scales of the activation and of the weight
     const float* sw;
@@ -53,7 +50,7 @@ struct StreamParams {
     int mpad;                  // the MMA's N: M rounded up to 16
     uint32_t idesc;
     int act, gated;
-    int prepared;
+    int prepared;              // weight scales: 1 = prepared blocks, 0 = 128x4 chunks
     int tiles, k_tiles, kchunks;
     int stages, stage_bytes;
     int w_early;               // the weight was complete before the previous kernel started
@@ -88,6 +85,7 @@ __device__ __forceinline__ void stream_step_w(uint32_t acc, uint64_t wd, uint64_
 template <bool I8>
 __global__ void __launch_bounds__(TTHREADS, 1)
 gemm_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const __grid_constant__ CUtensorMap tmSFW, const __grid_constant__ CUtensorMap tmSFX,
                    const StreamParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -123,23 +121,20 @@ gemm_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     const uint32_t tmem = *tmem_holder;
 
     // A stage: W box | scales of W | scales of x | x box.
-    auto load_w = [&](uint8_t* s, uint64_t* bar, int kt, int tile, int steps) {
-        tma_load_2d_w(s, &tmW, bar, kt * TKB, tile * TROWS);
-        if constexpr (!I8) {
-            const uint8_t* src = p.prepared
-                                     ? p.sfw + ((size_t)(tile >> 1) * p.k_tiles + kt) * 4096 + (tile & 1) * 2048
-                                     : p.sfw + ((size_t)tile * p.kchunks + 4 * kt) * 512;
-            bulk_load_w(s + TS_W, src, (uint32_t)steps * 512u, bar);
-        }
-    };
-    auto load_x = [&](uint8_t* s, uint64_t* bar, int kt, int steps) {
-        tma_load_2d_w(s + TS_W + (I8 ? 0 : 2 * TS_SF), &tmX, bar, kt * TKB, 0);
+    auto load_w = [&](int stage, int kt, int tile) {
+        uint8_t* s = smem + stage * p.stage_bytes;
+        tma_load_2d_w(s, &tmW, &full[stage], kt * TKB, tile * TROWS);
         if constexpr (!I8)
-            bulk_load_w(s + TS_W + TS_SF, p.sfx + (size_t)(4 * kt) * 512, (uint32_t)steps * 512u, bar);
+            tma_load_2d_w(s + TS_W, &tmSFW, &full[stage], 0,
+                          p.prepared ? ((tile >> 1) * p.k_tiles + kt) * 8 + (tile & 1) * 4
+                                     : tile * p.kchunks + 4 * kt);
     };
-    auto bytes_of = [&](int steps) -> uint32_t {
-        return TS_W + (uint32_t)p.mpad * TKB + (I8 ? 0u : 2u * (uint32_t)steps * 512u);
+    auto load_x = [&](int stage, int kt) {
+        uint8_t* s = smem + stage * p.stage_bytes;
+        tma_load_2d_w(s + TS_W + (I8 ? 0 : 2 * TS_SF), &tmX, &full[stage], kt * TKB, 0);
+        if constexpr (!I8) tma_load_2d_w(s + TS_W + TS_SF, &tmSFX, &full[stage], 0, 4 * kt);
     };
+    const uint32_t bytes = TS_W + (uint32_t)p.mpad * TKB + (I8 ? 0u : 2u * TS_SF);
     int n_early = 0;
     if (warp == 0) {
         if (lane == 0) {
@@ -149,9 +144,8 @@ gemm_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         if (p.w_early && (int)blockIdx.x < p.tiles) {
             n_early = min(p.stages, p.k_tiles);
             for (int i = 0; i < n_early; ++i) {
-                const int steps = min(4, p.kchunks - 4 * i);
-                mbar_arrive_expect_tx_w(&full[i], bytes_of(steps));
-                load_w(smem + i * p.stage_bytes, &full[i], i, (int)blockIdx.x, steps);
+                mbar_arrive_expect_tx_w(&full[i], bytes);
+                load_w(i, i, (int)blockIdx.x);
             }
         }
     }
@@ -164,18 +158,16 @@ gemm_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         bool ok = true;
         for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
             for (int kt = 0; kt < p.k_tiles; ++kt, ++fills) {
-                const int steps = min(4, p.kchunks - 4 * kt);
-                uint8_t* s = smem + stage * p.stage_bytes;
                 if (fills >= n_early) {
                     if (!mbar_wait_bounded_warp(&empty[stage], phase ^ 1, abort_flag, p.status,
                                                 p.budget_ns)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx_w(&full[stage], bytes_of(steps));
-                    load_w(s, &full[stage], kt, tile, steps);
+                    mbar_arrive_expect_tx_w(&full[stage], bytes);
+                    load_w(stage, kt, tile);
                 }
-                load_x(s, &full[stage], kt, steps);
+                load_x(stage, kt);
                 issued |= 1u << stage;
                 issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                 if (++stage == p.stages) {
@@ -191,7 +183,7 @@ gemm_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 mbar_wait_bounded(&full[s], (issued_phase >> s) & 1, &no_abort, p.status, p.budget_ns);
             }
     } else if (warp == 1) {
-        int stage = 0, slot = 0, it = 0;
+        int stage = 0, it = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x, ++it) {
@@ -209,20 +201,17 @@ gemm_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                     break;
                 }
                 tc_fence_after();
-                const int steps = min(4, p.kchunks - 4 * kt);
                 const uint32_t s = smem_u32(smem + stage * p.stage_bytes);
                 const uint64_t wd = sdesc_kmajor_sw128(s);
                 const uint64_t xd = sdesc_kmajor_sw128(s + TS_W + (I8 ? 0 : 2 * TS_SF));
                 const uint64_t sfw_d = sdesc_sf(s + TS_W), sfx_d = sdesc_sf(s + TS_W + TS_SF);
+                // Four steps to every stage, without a branch between them: past the end of K
+                // both operands are zero (as in gemm_pair.cu).
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    if (kk < steps) {
-                        stream_step_w<I8>(acc, wd + 2 * kk, xd + 2 * kk, p.idesc,
-                                          tmem + TTMEM_SF + 8u * (uint32_t)slot, sfw_d + 32 * kk,
-                                          sfx_d + 32 * kk, (kt > 0 || kk > 0) ? 1u : 0u);
-                        slot = slot == TSF_SLOTS - 1 ? 0 : slot + 1;
-                    }
-                }
+                for (int kk = 0; kk < 4; ++kk)
+                    stream_step_w<I8>(acc, wd + 2 * kk, xd + 2 * kk, p.idesc,
+                                      tmem + TTMEM_SF + 8u * (uint32_t)kk, sfw_d + 32 * kk,
+                                      sfx_d + 32 * kk, kk > 0 || kt > 0 ? 1u : 0u);
                 tc_commit_w(&empty[stage]);
                 if (++stage == p.stages) {
                     stage = 0;
@@ -315,8 +304,6 @@ nvfp4_status launch_stream_impl(const GemmActArgs& g, cudaStream_t stream) {
     }
     const int64_t kbytes = I8 ? g.K : g.K / 2;
     StreamParams p{};
-    p.sfw = g.sfb;
-    p.sfx = g.sfa;
     p.alpha = g.alpha;
     p.sx = g.sx;
     p.sw = g.sw;
@@ -342,12 +329,20 @@ nvfp4_status launch_stream_impl(const GemmActArgs& g, cudaStream_t stream) {
     p.w_early = g.weights_ready ? 1 : 0;
     p.status = status;
     p.budget_ns = 4000000000ull;   // 4 s
-    CUtensorMap mapW, mapX;
+    CUtensorMap mapW, mapX, mapSFW, mapSFX;
     if (!make_operand_map(&mapW, g.b, g.N, kbytes, TROWS) ||
         !make_operand_map(&mapX, g.a, g.M, kbytes, p.mpad))
         return NVFP4_ERR_CUDA;
+    mapSFW = mapSFX = mapX;                    // unused by int8
+    if (!I8) {
+        const int64_t w_chunks = p.prepared ? (g.N + 255) / 256 * p.k_tiles * 8
+                                            : (g.N + 127) / 128 * p.kchunks;
+        if (!make_scale_map(&mapSFW, g.sfb, w_chunks) || !make_scale_map(&mapSFX, g.sfa, p.kchunks))
+            return NVFP4_ERR_CUDA;
+    }
     const unsigned grid = (unsigned)(p.tiles < dev.sms ? p.tiles : dev.sms);
-    return launch_pdl(gemm_stream_kernel<I8>, grid, TTHREADS, TSMEM, stream, mapW, mapX, p) == cudaSuccess
+    return launch_pdl(gemm_stream_kernel<I8>, grid, TTHREADS, TSMEM, stream, mapW, mapX, mapSFW, mapSFX,
+                      p) == cudaSuccess
                ? NVFP4_OK
                : NVFP4_ERR_CUDA;
 }

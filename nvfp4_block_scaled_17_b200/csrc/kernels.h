@@ -143,6 +143,10 @@ constexpr int64_t kStreamMaxRows = 64;
 nvfp4_status launch_gemm_stream(const GemmActArgs& g, cudaStream_t stream);
 nvfp4_status launch_gemm_act_split_k(const GemmActArgs& g, bool* taken, cudaStream_t stream);
 
+// 512-byte scale chunks (of a 128x4 or prepared layout) as the rows of a 2-D tensor map of
+// 32-bit words, four rows per load; rows past `chunks` read as zero.
+bool make_scale_map(CUtensorMap* map, const void* base, int64_t chunks);
+
 // bf16 [M, N] tensor map with a 32 x 32 box and 64-byte swizzle (N % 8 == 0).
 bool make_output_map(CUtensorMap* map, void* base, int64_t M, int64_t N);
 
