@@ -144,30 +144,26 @@ __device__ __forceinline__ void small_step_w(uint32_t acc0, uint32_t acc1, uint6
 }
 
 // The int8 form of a K step (K = 32): no scales, both MMAs under one election.
-template <bool TWO>
 __device__ __forceinline__ void small_step_i8_w(uint32_t acc0, uint32_t acc1, uint64_t wd,
                                                 uint64_t xd, uint32_t idesc, uint32_t accumulate) {
-    if constexpr (TWO) {
-        asm volatile(
-            "{\n\t"
-            ".reg .pred p, e;\n\t"
-            ".reg .b64 w1;\n\t"
-            "elect.sync _|e, 0xffffffff;\n\t"
-            "setp.ne.b32 p, %5, 0;\n\t"
-            "add.u64 w1, %2, 1024;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::i8 [%0], %2, %3, %4, p;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::i8 [%1], w1, %3, %4, p;\n\t"
-            "}" ::"r"(acc0),
-            "r"(acc1), "l"(wd), "l"(xd), "r"(idesc), "r"(accumulate)
-            : "memory");
-    } else {
-        mma_i8_w(acc0, wd, xd, idesc, accumulate);
-    }
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p, e;\n\t"
+        ".reg .b64 w1;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "add.u64 w1, %2, 1024;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::i8 [%0], %2, %3, %4, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::i8 [%1], w1, %3, %4, p;\n\t"
+        "}" ::"r"(acc0),
+        "r"(acc1), "l"(wd), "l"(xd), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 template <bool RSB, bool F32, bool I8 = false, bool ACT = false>
 __global__ void __launch_bounds__(XTHREADS, 1)
 gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                  const __grid_constant__ CUtensorMap tmSFW, const __grid_constant__ CUtensorMap tmSFX,
                   const SmallParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -211,6 +207,12 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         uint8_t* sSFW = sW + XS_W + XS_X;
         tma_load_2d_w(sW, &tmW, &full[stage], kt * XBKB, tile * XW_ROWS);
         if constexpr (I8) return;
+        if constexpr (ACT) {   // both row tiles' four chunks each, zeros past the last ones
+            const int at = RSB ? (tile * p.k_tiles + kt) * 8 : 2 * tile * p.kchunks + 4 * kt;
+            tma_load_2d_w(sSFW, &tmSFW, &full[stage], 0, at);
+            tma_load_2d_w(sSFW + 2048, &tmSFW, &full[stage], 0, at + (RSB ? 4 : p.kchunks));
+            return;
+        }
         if constexpr (RSB) {
             bulk_load_w(sSFW, p.sfw + ((size_t)tile * p.k_tiles + kt) * 4096, 4096u, &full[stage]);
         } else {
@@ -222,6 +224,7 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     };
     auto stage_bytes = [&](int steps) -> uint32_t {
         if constexpr (I8) return XS_W + (uint32_t)p.mpad * XBKB;
+        if constexpr (ACT) return XS_W + (uint32_t)p.mpad * XBKB + XS_SFW + XS_SFX;
         const uint32_t sfx_bytes = (uint32_t)steps * 512u;
         const uint32_t sfw_bytes = RSB ? 4096u : sfx_bytes * (two ? 2u : 1u);
         return XS_W + (uint32_t)p.mpad * XBKB + sfw_bytes + sfx_bytes;
@@ -267,7 +270,9 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 uint8_t* sSFX = sX + XS_X + XS_SFW;
                 const uint32_t sfx_bytes = (uint32_t)steps * 512u;
                 tma_load_2d_w(sX, &tmX, &full[stage], kt * XBKB, 0);
-                if constexpr (!I8)
+                if constexpr (ACT && !I8)
+                    tma_load_2d_w(sSFX, &tmSFX, &full[stage], 0, 4 * kt);
+                else if constexpr (!I8)
                     bulk_load_w(sSFX, p.sfx + (size_t)(4 * kt) * 512, sfx_bytes, &full[stage]);
                 issued |= 1u << stage;
                 issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
@@ -296,8 +301,7 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                     break;
                 }
                 tc_fence_after();
-                // (int8: four steps always; past the end of K both operands are zero)
-                const int steps = I8 ? 4 : min(4, p.kchunks - 4 * kt);
+                const int steps = min(4, p.kchunks - 4 * kt);
                 // the stage's descriptors; step kk adds 32 bytes to W and x (2 units) and
                 // 512 to the scale chunks (32 units).  Both weight scale layouts leave the
                 // stage's chunks in the same shared-memory order.
@@ -306,25 +310,34 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 const uint64_t xd = sdesc_kmajor_sw128(w0 + XS_W);
                 const uint64_t sfw_d = sdesc_sf(w0 + XS_W + XS_X);
                 const uint64_t sfx_d = sdesc_sf(w0 + XS_W + XS_X + XS_SFW);
+                if constexpr (ACT) {
+                    // Four steps of both row tiles to every stage, without a branch between
+                    // them: past the end of K, and in rows past the last, the operands are zero
+                    // (as in gemm_pair.cu).
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    if (kk < steps) {
-                        const uint32_t sf_t = tmem + XTMEM_SF + 12u * (uint32_t)slot;
-                        const uint32_t acc = (kt > kt_begin || kk > 0) ? 1u : 0u;
-                        if constexpr (I8) {
-                            if (two)
-                                small_step_i8_w<true>(tmem, tmem + XTMEM_ACC1, wd + 2 * kk,
-                                                      xd + 2 * kk, p.idesc, acc);
-                            else
-                                small_step_i8_w<false>(tmem, tmem + XTMEM_ACC1, wd + 2 * kk,
-                                                       xd + 2 * kk, p.idesc, acc);
-                        } else if (two)
-                            small_step_w<true>(tmem, tmem + XTMEM_ACC1, wd + 2 * kk, xd + 2 * kk,
-                                               p.idesc, sf_t, sfw_d + 32 * kk, sfx_d + 32 * kk, acc);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t acc = kk > 0 || kt > kt_begin ? 1u : 0u;
+                        if constexpr (I8)
+                            small_step_i8_w(tmem, tmem + XTMEM_ACC1, wd + 2 * kk, xd + 2 * kk, p.idesc, acc);
                         else
-                            small_step_w<false>(tmem, tmem + XTMEM_ACC1, wd + 2 * kk, xd + 2 * kk,
-                                                p.idesc, sf_t, sfw_d + 32 * kk, sfx_d + 32 * kk, acc);
-                        slot = slot == XSF_SLOTS - 1 ? 0 : slot + 1;
+                            small_step_w<true>(tmem, tmem + XTMEM_ACC1, wd + 2 * kk, xd + 2 * kk,
+                                               p.idesc, tmem + XTMEM_SF + 12u * (uint32_t)kk,
+                                               sfw_d + 32 * kk, sfx_d + 32 * kk, acc);
+                    }
+                } else {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk < steps) {
+                            const uint32_t sf_t = tmem + XTMEM_SF + 12u * (uint32_t)slot;
+                            const uint32_t acc = (kt > kt_begin || kk > 0) ? 1u : 0u;
+                            if (two)
+                                small_step_w<true>(tmem, tmem + XTMEM_ACC1, wd + 2 * kk, xd + 2 * kk,
+                                                   p.idesc, sf_t, sfw_d + 32 * kk, sfx_d + 32 * kk, acc);
+                            else
+                                small_step_w<false>(tmem, tmem + XTMEM_ACC1, wd + 2 * kk, xd + 2 * kk,
+                                                    p.idesc, sf_t, sfw_d + 32 * kk, sfx_d + 32 * kk, acc);
+                            slot = slot == XSF_SLOTS - 1 ? 0 : slot + 1;
+                        }
                     }
                 }
                 tc_commit_w(&empty[stage]);
@@ -497,6 +510,15 @@ nvfp4_status launch_small_impl(const uint8_t* a, const uint8_t* sfa, const uint8
     CUtensorMap mapW, mapX;
     if (!make_operand_map(&mapW, b, N, kbytes, XW_ROWS) || !make_operand_map(&mapX, a, M, kbytes, p.mpad))
         return NVFP4_ERR_CUDA;
+    p.k_tiles = (int)((kbytes + XBKB - 1) / XBKB);
+    p.kchunks = (int)(kbytes / 32);          // 32-byte MMA K steps
+    CUtensorMap mapSFW = mapX, mapSFX = mapX;   // the activation builds' scale loads (FP4)
+    if (ACT && !I8) {
+        const int64_t w_chunks = RSB ? (N + XW_ROWS - 1) / XW_ROWS * p.k_tiles * 8
+                                     : (N + 127) / 128 * p.kchunks;
+        if (!make_scale_map(&mapSFW, sfb, w_chunks) || !make_scale_map(&mapSFX, sfa, p.kchunks))
+            return NVFP4_ERR_CUDA;
+    }
     p.sfw = sfb;
     p.sfx = sfa;
     p.alpha = alpha;
@@ -508,8 +530,6 @@ nvfp4_status launch_small_impl(const uint8_t* a, const uint8_t* sfa, const uint8
     // E2M1 x E2M1, UE4M3 block scales, both K-major; N = padded M, M = 128.  int8: signed
     // operands (format 1 both), int32 accumulator (D format 2).
     p.idesc = (I8 ? 2u << 4 : 0u) | (1u << 7) | (1u << 10) | ((uint32_t)(p.mpad >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-    p.k_tiles = (int)((kbytes + XBKB - 1) / XBKB);
-    p.kchunks = (int)(kbytes / 32);          // 32-byte MMA K steps
     p.w_row_tiles = (int)((N + 127) / 128);
     p.w_early = weights_ready ? 1 : 0;
     p.sx = sx;
@@ -526,7 +546,7 @@ nvfp4_status launch_small_impl(const uint8_t* a, const uint8_t* sfa, const uint8
     p.splits = small_splits<RSB, F32, I8, ACT>(tiles, p.k_tiles, dev);
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = small_config(tiles * p.splits, p.splits, stream, attr);
-    if (cudaLaunchKernelEx(&cfg, gemm_small_kernel<RSB, F32, I8, ACT>, mapW, mapX, p) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, gemm_small_kernel<RSB, F32, I8, ACT>, mapW, mapX, mapSFW, mapSFX, p) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     return NVFP4_OK;
 }
