@@ -350,9 +350,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         break;
                     }
                     tc_fence_after();
-                    // (int8 with an activation: four steps to every stage, without a branch
-                    // between them; past the end of K both operands are zero)
-                    const int steps = I8 && ACT ? 4 : min(4, p.kchunks - 4 * kt);
+                    const int steps = min(4, p.kchunks - 4 * kt);
                     // Descriptors of the stage's first K step; step kk adds 32 bytes to the
                     // A and B start addresses and 512 to the scale chunks' (2 and 32 in the
                     // descriptors' address fields).  B's second 128-row half is 2048 bytes
