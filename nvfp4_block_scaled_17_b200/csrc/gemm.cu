@@ -979,15 +979,14 @@ nvfp4_status gemm_act_split_k(const GemmActArgs& g, bool* taken, cudaStream_t st
     const int64_t m_blocks = (g.M + BM - 1) / BM, n_blocks = (g.N + BN - 1) / BN;
     if (m_blocks * n_blocks * 2 > dev.sms) return NVFP4_OK;
     const int tiles = (int)(m_blocks * n_blocks), k_tiles = (int)((kbytes + BKB - 1) / BKB);
-    // Splitting K saves mainloop time, 0.45 us per stage of K not run in sequence, and costs
-    // the exchange of the partial tiles, 5 to 8 us.  Against SM pairs without a split, us:
-    // 512 x 1024 x 5120 FP4 (S = 8, 20 stages) 12.9 : 17.9, 1024 x 1024 x 5120 (S = 4) 14.7 :
-    // 18.0, 300 x 520 x 576 int8 (S = 5, 5 stages) 10.9 : 12.1; but 512 x 4096 x 4096 (S = 2)
-    // 21.0 : 16.9, 256 x 1024 x 1024 FP4 (S = 4, 4 stages) 12.0 : 10.8, 300 x 520 x 576 FP4
-    // (S = 3, 3 stages) 14.0 : 10.7.
-    if (k_tiles < 5) return NVFP4_OK;
+    // Splitting K saves the stages of K that no longer run in sequence, 0.35 us each, and costs
+    // the exchange of the partial tiles, 3 to 7 us.  Against SM pairs without a split, us:
+    // 64 x 1024 x 5120 FP4 (S = 8, 20 stages) 8.8 : 15.4, 1024 x 1024 x 5120 (S = 4) 14.6 :
+    // 15.6, 300 x 520 x 2624 (S = 8, 11 stages) 10.8 : 12.1; but 512 x 1024 x 2048 (S = 8, 8
+    // stages) 11.9 : 10.8, 1024 x 1024 x 2560 (S = 4, 10 stages) 13.6 : 11.7, 256 x 5120 x 5120
+    // (S = 3) 17.9 : 16.3, 512 x 4096 x 4096 (S = 2) 21.9 : 15.1.
     const int splits = choose_splits<I8, RSB, false, true>(tiles, k_tiles, dev);
-    if (splits < 4) return NVFP4_OK;
+    if (splits < 4 || k_tiles - k_tiles / splits < 9) return NVFP4_OK;
     *taken = true;
     int* status = nullptr;
     if ((st = status_word(&status)) != NVFP4_OK) return st;
