@@ -99,6 +99,17 @@ __device__ __forceinline__ void tma_load_2d_pair_w(uint32_t dst, const CUtensorM
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d_pair_w(uint32_t dst, const CUtensorMap* map,
+                                                   uint32_t leader_bar, int32_t x, int32_t y,
+                                                   int32_t z) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(leader_bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 // Completion of all earlier MMAs and scale copies, to the barrier at this offset in both CTAs.
 __device__ __forceinline__ void commit_both_w(uint64_t* bar) {
     asm volatile(
@@ -289,16 +300,19 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         if constexpr (!I8) {
             // 512-byte scale chunks of the tile's 128-row halves, four K steps each
             const int h = w.n0 >> 7, n_blk = w.n0 >> 8;
-            const int at = p.prepared ? (n_blk * p.k_tiles + kt) * 8 + (h & 1) * 4 : h * p.kchunks + 4 * kt;
-            tma_load_2d_pair_w(sf, &tmSFB, bar, 0, at);
-            if (!w.half) tma_load_2d_pair_w(sf + 2048, &tmSFB, bar, 0, at + (p.prepared ? 4 : p.kchunks));
+            const int at = p.prepared ? (n_blk * p.k_tiles + kt) * 8 + (h & 1) * 4 : 4 * kt;
+            const int tile = p.prepared ? 0 : h;
+            tma_load_3d_pair_w(sf, &tmSFB, bar, 0, at, tile);
+            if (!w.half)
+                tma_load_3d_pair_w(sf + 2048, &tmSFB, bar, 0, at + (p.prepared ? 4 : 0),
+                                   tile + (p.prepared ? 0 : 1));
         }
     };
     auto load_a = [&](int stage, int kt, const Item& w) {
         const uint32_t s = smem_u32(smem + stage * SM::STAGE), bar = full0 + 8u * (uint32_t)stage;
         tma_load_2d_pair_w(s, &tmA, bar, kt * PKB, w.m_blk * 2 * PROWS + rank * PROWS);
         if constexpr (!I8)
-            tma_load_2d_pair_w(s + 2 * PS_OP, &tmSFA, bar, 0, (2 * w.m_blk + rank) * p.kchunks + 4 * kt);
+            tma_load_3d_pair_w(s + 2 * PS_OP, &tmSFA, bar, 0, 4 * kt, 2 * w.m_blk + rank);
     };
     // both CTAs' bytes of a stage
     auto stage_bytes = [&](const Item& w) -> uint32_t {
@@ -669,15 +683,14 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 
 }  // namespace
 
-// 512-byte scale chunks as the rows of a 2-D tensor of 32-bit words, four rows per load.
-bool make_scale_map(CUtensorMap* map, const void* base, int64_t chunks) {
+bool make_scale_map(CUtensorMap* map, const void* base, int64_t chunks, int64_t tiles) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
-    cuuint64_t dims[2] = {128, (cuuint64_t)chunks};
-    cuuint64_t strides[1] = {512};
-    cuuint32_t box[2] = {128, 4};
-    cuuint32_t estr[2] = {1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+    cuuint64_t dims[3] = {128, (cuuint64_t)chunks, (cuuint64_t)tiles};
+    cuuint64_t strides[2] = {512, (cuuint64_t)chunks * 512};
+    cuuint32_t box[3] = {128, 4, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 3, const_cast<void*>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -755,10 +768,9 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
         return NVFP4_ERR_CUDA;
     mapSFA = mapSFB = mapY = mapA;             // where unused
     if (!I8) {
-        const int64_t b_chunks = p.prepared ? (int64_t)p.n_blocks * p.k_tiles * 8
-                                            : (g.N + 127) / 128 * p.kchunks;
-        if (!make_scale_map(&mapSFA, g.sfa, (g.M + 127) / 128 * p.kchunks) ||
-            !make_scale_map(&mapSFB, g.sfb, b_chunks))
+        if (!make_scale_map(&mapSFA, g.sfa, p.kchunks, (g.M + 127) / 128) ||
+            !(p.prepared ? make_scale_map(&mapSFB, g.sfb, (int64_t)p.n_blocks * p.k_tiles * 8, 1)
+                         : make_scale_map(&mapSFB, g.sfb, p.kchunks, (g.N + 127) / 128)))
             return NVFP4_ERR_CUDA;
     }
     if (p.tma_store && !make_output_map(&mapY, g.y, g.M, p.n_out)) return NVFP4_ERR_CUDA;
@@ -795,9 +807,9 @@ nvfp4_status launch_gemm_act(const GemmActArgs& g, cudaStream_t stream) {
     if (st != NVFP4_OK) return st;
     // A weight whose 256-row tiles leave no SMs to split K over streams through all SMs for up
     // to 32 rows, and for up to 64 when K is long enough (20 stages) to cover the stream
-    // kernel's narrow stores.  Against SM pairs, us: 51200 x 5120 FP4 at 1 row 31 : 42, 64 rows
-    // 37 : 42, 128 rows 48 : 43; 20480 x 2560 FP4 (10 stages) 32 rows 14.5 : 17.7, 64 rows
-    // 18.7 : 17.3; 19456 x 512 int8 32 rows 9.3 : 10.9, 48 rows 12.3 : 11.0.
+    // kernel's narrow stores.  Against SM pairs, us: 51200 x 5120 FP4 at 1 row 28.2 : 45.8, 64
+    // rows 31.9 : 35.4; 20480 x 2560 FP4 (10 stages) 32 rows 11.4 : 13.7, 48 rows 13.0 : 14.1,
+    // 64 rows 15.1 : 13.9; 19456 x 512 int8 32 rows 7.6 : 9.3, 48 rows 10.0 : 9.4.
     const bool long_weight = (g.N + 255) / 256 * 2 > dev.sms;
     const int64_t stages = ((g.int8 ? g.K : g.K / 2) + 127) / 128;
     if (long_weight && (g.M <= kSmallMaxRows || (g.M <= kStreamMaxRows && stages >= 20)))

@@ -30,6 +30,9 @@
 //     tile over the S partials in rank order (distributed shared memory) and applies
 //     alpha and the bias: deterministic, and the unrounded-output build (F32) stores
 //     the same fp32 value the bf16 build rounds.
+// The ACT builds put gemm_stream.cu's epilogue (activation, gate, residual) after that sum
+// and also come for int8, whose partial sums are integers; their K steps are issued four to
+// a stage without a branch, past the end of K on zeros, and their scales come by tensor map.
 // With weights_ready (the linear paths) the weight copies of the first stages go out
 // before the wait for the previous kernel, so the weight stream overlaps the activation
 // quantizer; the activation's copies follow the wait.
@@ -208,9 +211,9 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         tma_load_2d_w(sW, &tmW, &full[stage], kt * XBKB, tile * XW_ROWS);
         if constexpr (I8) return;
         if constexpr (ACT) {   // both row tiles' four chunks each, zeros past the last ones
-            const int at = RSB ? (tile * p.k_tiles + kt) * 8 : 2 * tile * p.kchunks + 4 * kt;
-            tma_load_2d_w(sSFW, &tmSFW, &full[stage], 0, at);
-            tma_load_2d_w(sSFW + 2048, &tmSFW, &full[stage], 0, at + (RSB ? 4 : p.kchunks));
+            const int at = RSB ? (tile * p.k_tiles + kt) * 8 : 4 * kt;
+            tma_load_3d_w(sSFW, &tmSFW, &full[stage], 0, at, RSB ? 0 : 2 * tile);
+            tma_load_3d_w(sSFW + 2048, &tmSFW, &full[stage], 0, at + (RSB ? 4 : 0), RSB ? 0 : 2 * tile + 1);
             return;
         }
         if constexpr (RSB) {
@@ -271,7 +274,7 @@ gemm_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 const uint32_t sfx_bytes = (uint32_t)steps * 512u;
                 tma_load_2d_w(sX, &tmX, &full[stage], kt * XBKB, 0);
                 if constexpr (ACT && !I8)
-                    tma_load_2d_w(sSFX, &tmSFX, &full[stage], 0, 4 * kt);
+                    tma_load_3d_w(sSFX, &tmSFX, &full[stage], 0, 4 * kt, 0);
                 else if constexpr (!I8)
                     bulk_load_w(sSFX, p.sfx + (size_t)(4 * kt) * 512, sfx_bytes, &full[stage]);
                 issued |= 1u << stage;
@@ -514,9 +517,9 @@ nvfp4_status launch_small_impl(const uint8_t* a, const uint8_t* sfa, const uint8
     p.kchunks = (int)(kbytes / 32);          // 32-byte MMA K steps
     CUtensorMap mapSFW = mapX, mapSFX = mapX;   // the activation builds' scale loads (FP4)
     if (ACT && !I8) {
-        const int64_t w_chunks = RSB ? (N + XW_ROWS - 1) / XW_ROWS * p.k_tiles * 8
-                                     : (N + 127) / 128 * p.kchunks;
-        if (!make_scale_map(&mapSFW, sfb, w_chunks) || !make_scale_map(&mapSFX, sfa, p.kchunks))
+        const int64_t w_chunks = RSB ? (N + XW_ROWS - 1) / XW_ROWS * p.k_tiles * 8 : p.kchunks;
+        if (!make_scale_map(&mapSFW, sfb, w_chunks, RSB ? 1 : (N + 127) / 128) ||
+            !make_scale_map(&mapSFX, sfa, p.kchunks, 1))
             return NVFP4_ERR_CUDA;
     }
     p.sfw = sfb;

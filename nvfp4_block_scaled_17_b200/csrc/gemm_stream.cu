@@ -4,10 +4,11 @@
 // With M <= 64 rows the call is the weight's one trip from HBM (N x K bytes, or 9/16 of them
 // for FP4), so the design keeps that stream going: one persistent CTA per SM walks tiles of
 // 128 weight rows, and its copies run ahead across tile boundaries, as many stages as shared
-// memory holds (nine of 22 KiB at M = 16).  The operands are swapped as in gemm_small.cu: the
+// memory holds (ten of 22 KiB at M = 16).  The operands are swapped as in gemm_small.cu: the
 // weight rows fill the MMA's M = 128, the activation rows (to a multiple of 16) its N.
 // 51200 x 5120 FP4 for one token: 147 MB, 22.6 us at the measured copy rate; the cluster
-// kernel, one tile of 256 rows per CTA and no split left, ran it as 1.35 waves in 38.7 us.
+// kernel, one tile of 256 rows per CTA and no split left, ran it as 1.35 waves in 38.7 us;
+// this one takes 28.2 us, 0.80 of that rate (int8 42.6 us), of which 3 us are start and end.
 //
 //   warp 0      TMA producer: per stage (128 bytes of K) the 128-row weight box and its scale
 //               chunks, the activation box and its chunks.
@@ -125,14 +126,14 @@ gemm_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         uint8_t* s = smem + stage * p.stage_bytes;
         tma_load_2d_w(s, &tmW, &full[stage], kt * TKB, tile * TROWS);
         if constexpr (!I8)
-            tma_load_2d_w(s + TS_W, &tmSFW, &full[stage], 0,
-                          p.prepared ? ((tile >> 1) * p.k_tiles + kt) * 8 + (tile & 1) * 4
-                                     : tile * p.kchunks + 4 * kt);
+            tma_load_3d_w(s + TS_W, &tmSFW, &full[stage], 0,
+                          p.prepared ? ((tile >> 1) * p.k_tiles + kt) * 8 + (tile & 1) * 4 : 4 * kt,
+                          p.prepared ? 0 : tile);
     };
     auto load_x = [&](int stage, int kt) {
         uint8_t* s = smem + stage * p.stage_bytes;
         tma_load_2d_w(s + TS_W + (I8 ? 0 : 2 * TS_SF), &tmX, &full[stage], kt * TKB, 0);
-        if constexpr (!I8) tma_load_2d_w(s + TS_W + TS_SF, &tmSFX, &full[stage], 0, 4 * kt);
+        if constexpr (!I8) tma_load_3d_w(s + TS_W + TS_SF, &tmSFX, &full[stage], 0, 4 * kt, 0);
     };
     const uint32_t bytes = TS_W + (uint32_t)p.mpad * TKB + (I8 ? 0u : 2u * TS_SF);
     int n_early = 0;
@@ -335,9 +336,9 @@ nvfp4_status launch_stream_impl(const GemmActArgs& g, cudaStream_t stream) {
         return NVFP4_ERR_CUDA;
     mapSFW = mapSFX = mapX;                    // unused by int8
     if (!I8) {
-        const int64_t w_chunks = p.prepared ? (g.N + 255) / 256 * p.k_tiles * 8
-                                            : (g.N + 127) / 128 * p.kchunks;
-        if (!make_scale_map(&mapSFW, g.sfb, w_chunks) || !make_scale_map(&mapSFX, g.sfa, p.kchunks))
+        if (!(p.prepared ? make_scale_map(&mapSFW, g.sfb, (g.N + 255) / 256 * p.k_tiles * 8, 1)
+                         : make_scale_map(&mapSFW, g.sfb, p.kchunks, p.tiles)) ||
+            !make_scale_map(&mapSFX, g.sfa, p.kchunks, 1))
             return NVFP4_ERR_CUDA;
     }
     const unsigned grid = (unsigned)(p.tiles < dev.sms ? p.tiles : dev.sms);

@@ -143,9 +143,12 @@ constexpr int64_t kStreamMaxRows = 64;
 nvfp4_status launch_gemm_stream(const GemmActArgs& g, cudaStream_t stream);
 nvfp4_status launch_gemm_act_split_k(const GemmActArgs& g, bool* taken, cudaStream_t stream);
 
-// 512-byte scale chunks (of a 128x4 or prepared layout) as the rows of a 2-D tensor map of
-// 32-bit words, four rows per load; rows past `chunks` read as zero.
-bool make_scale_map(CUtensorMap* map, const void* base, int64_t chunks);
+// 512-byte scale chunks as the rows of a 3-D tensor map of 32-bit words, [tiles][chunks][128],
+// four chunks per load: of a 128x4 layout its row tiles and K steps, of a prepared layout one
+// tile of all its chunks.  Chunks past a tile's last and tiles past the last read as zero, so
+// the steps past the end of K meet no other rows' scales (a NaN there would spread to rows
+// that have none: 0 * NaN).
+bool make_scale_map(CUtensorMap* map, const void* base, int64_t chunks, int64_t tiles);
 
 // bf16 [M, N] tensor map with a 32 x 32 box and 64-byte swizzle (N % 8 == 0).
 bool make_output_map(CUtensorMap* map, void* base, int64_t M, int64_t N);
