@@ -327,7 +327,8 @@ NVFP4_API nvfp4_status int8_linear(const void* x_bf16, int64_t M, int64_t K, con
  *   eps          : host value, finite and > 0
  *   residual_out : out, bf16 [rows, K] = h, or NULL; needs a residual; may equal x or
  *                  residual (in place)
- *   norm_out     : out, bf16 [rows, K] = n, or NULL; may not overlap the inputs
+ *   norm_out     : out, bf16 [rows, K] = n, or NULL
+ * Apart from residual_out's in-place forms, no output may overlap another tensor.
  */
 
 /*
@@ -382,7 +383,7 @@ NVFP4_API nvfp4_status nvfp4_rmsnorm_quantize(const void* x_bf16, const void* re
  *                   the up projection's row j (bias likewise), N even
  *   residual_bf16 : in,  bf16 [M, n_out] or NULL; may equal y (in place), otherwise may not
  *                   overlap it
- *   y_bf16        : out, bf16 [M, n_out]
+ *   y_bf16        : out, bf16 [M, n_out]; overlaps no other tensor
  * int8: K <= 131040, so that every sum of code products is exact in 32 bits.
  * Errors: INVALID_ARG (also an unknown activation, sfb_prepared not 0 or 1), SHAPE (also
  * gated with N odd), ALIGN (also residual 16-byte), DEVICE, CUDA.
@@ -400,7 +401,7 @@ NVFP4_API nvfp4_status int8_gemm_act(const int8_t* a, const float* sa, const int
 /*
  * nvfp4_linear_act, int8_linear_act -- nvfp4_linear (nvfp4_linear_prepared with
  * w_sf_prepared = 1) and int8_linear ending in the same epilogue; arguments, workspace and
- * errors otherwise as theirs.
+ * errors otherwise as theirs.  y may be x itself (N = K): x is read before y is written.
  */
 NVFP4_API nvfp4_status nvfp4_linear_act(const void* x_bf16, int64_t M, int64_t K,
                                         const uint8_t* w_packed, const uint8_t* w_sf,

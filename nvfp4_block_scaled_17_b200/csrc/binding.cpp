@@ -77,7 +77,25 @@ void* need_bytes(const at::Tensor* t, const char* name, int64_t least, const at:
     return t->data_ptr();
 }
 
-// Whether two buffers share bytes without starting at the same one.
+// The address of a float32 tensor of one element, of whatever shape.
+void* need_scalar(const at::Tensor* t, const char* name, const at::Tensor& like) {
+    if (!t) return nullptr;
+    if (t->scalar_type() != at::kFloat)
+        throw type_error(std::string(name) + " must be a " + c10::toString(at::kFloat) + " tensor");
+    if (t->numel() != 1) throw value_error(std::string(name) + " must be a tensor of one element");
+    if (t->device() != like.device())
+        throw type_error(std::string(name) + " must be on " + like.device().str());
+    return t->data_ptr();
+}
+
+// A buffer and its name in a refusal.
+struct Named {
+    const char* name;
+    const void* p;
+    int64_t bytes;
+};
+
+// Whether two buffers share bytes.
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
     const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return a && b && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
@@ -164,12 +182,26 @@ NormArgs norm_args(PyObject* x, PyObject* weight, PyObject* residual, PyObject* 
     return a;
 }
 
+void codes_apart(const NormArgs& a, const Named& codes, const Named& scales) {
+    const int64_t bytes = 2 * a.R * a.K;
+    for (const Named* o : {&codes, &scales}) {
+        for (const void* t : {a.px, a.residual, a.h, a.n})
+            if (overlap(o->p, o->bytes, t, bytes))
+                throw value_error(std::string(o->name) + " must not overlap the other tensors");
+        if (overlap(o->p, o->bytes, a.weight, 2 * a.K))
+            throw value_error(std::string(o->name) + " must not overlap the other tensors");
+    }
+    if (overlap(codes.p, codes.bytes, scales.p, scales.bytes))
+        throw value_error(std::string(scales.name) + " must not overlap the other tensors");
+}
+
 // (x, weight, eps, residual, codes, scales, residual_out, norm_out, stream)
 PyObject* py_int8_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     return guarded(n, 9, [&]() -> int {
         const NormArgs a = norm_args(v[0], v[1], v[3], v[6], v[7]);
         void* q = need(tensor(v[4], "codes"), "codes", at::kChar, {a.R, a.K}, *a.x);
         void* s = need(tensor(v[5], "scales"), "scales", at::kFloat, {a.R}, *a.x);
+        codes_apart(a, {"codes", q, a.R * a.K}, {"scales", s, 4 * a.R});
         const double eps = number(v[2], "eps");
         on_current_device(*a.x, "x");
         if (a.R == 0) return NVFP4_OK;           // an empty tensor has no address
@@ -182,11 +214,13 @@ PyObject* py_int8_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
 PyObject* py_nvfp4_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     return guarded(n, 12, [&]() -> int {
         const NormArgs a = norm_args(v[0], v[1], v[3], v[9], v[10]);
-        void* gsf = need(tensor(v[4], "gsf"), "gsf", at::kFloat, {1}, *a.x);
+        void* gsf = need_scalar(tensor(v[4], "gsf"), "gsf", *a.x);
         void* packed = need(tensor(v[5], "packed"), "packed", at::kByte, {a.R, a.K / 2}, *a.x);
-        void* sf = need_bytes(tensor(v[6], "scales"), "scales", (int64_t)entries.scale_bytes(a.R, a.K), *a.x);
-        void* gsf_w = need(tensor(v[7], "gsf_w", true), "gsf_w", at::kFloat, {1}, *a.x);
-        void* alpha = need(tensor(v[8], "alpha_out", true), "alpha_out", at::kFloat, {1}, *a.x);
+        const int64_t sf_bytes = (int64_t)entries.scale_bytes(a.R, a.K);
+        void* sf = need_bytes(tensor(v[6], "scales"), "scales", sf_bytes, *a.x);
+        codes_apart(a, {"packed", packed, a.R * (a.K / 2)}, {"scales", sf, sf_bytes});
+        void* gsf_w = need_scalar(tensor(v[7], "gsf_w", true), "gsf_w", *a.x);
+        void* alpha = need_scalar(tensor(v[8], "alpha_out", true), "alpha_out", *a.x);
         const double eps = number(v[2], "eps");
         on_current_device(*a.x, "x");
         if (a.R == 0) return NVFP4_OK;
@@ -217,9 +251,21 @@ EpilogueArgs epilogue_args(PyObject* bias, PyObject* act, PyObject* residual, Py
     return e;
 }
 
-void not_over(const EpilogueArgs& e, int64_t M, int64_t N, const void* p, int64_t bytes, const char* name) {
+void not_over(const EpilogueArgs& e, int64_t M, int64_t N, std::initializer_list<Named> operands) {
     const int64_t cols = (e.act & NVFP4_ACT_GATED) ? N / 2 : N;
-    if (overlap(e.y, 2 * M * cols, p, bytes)) throw value_error(std::string("out must not overlap ") + name);
+    for (const Named& o : operands)
+        if (overlap(e.y, 2 * M * cols, o.p, o.bytes))
+            throw value_error(std::string("out must not overlap ") + o.name);
+    if (overlap(e.y, 2 * M * cols, e.bias, 2 * N)) throw value_error("out must not overlap bias");
+}
+
+// A linear's workspace holds x's codes while out is written.
+void workspace_apart(const EpilogueArgs& e, int64_t M, int64_t N, const at::Tensor& x, const at::Tensor& ws) {
+    const int64_t cols = (e.act & NVFP4_ACT_GATED) ? N / 2 : N;
+    if (overlap(ws.data_ptr(), ws.numel(), x.data_ptr(), 2 * x.numel()))
+        throw value_error("workspace must not overlap x");
+    if (overlap(ws.data_ptr(), ws.numel(), e.residual, 2 * M * cols))
+        throw value_error("workspace must not overlap residual");
 }
 
 // (a, sa, b, sb, bias, activation, residual, out, stream)
@@ -232,7 +278,7 @@ PyObject* py_int8_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
         void* sa = need(tensor(v[1], "sa"), "sa", at::kFloat, {M}, a);
         void* sb = need(tensor(v[3], "sb"), "sb", at::kFloat, {N}, a);
         const EpilogueArgs e = epilogue_args(v[4], v[5], v[6], v[7], M, N, a);
-        not_over(e, M, N, a.data_ptr(), M * K, "a");
+        not_over(e, M, N, {{"a", a.data_ptr(), M * K}, {"b", pb, N * K}, {"sa", sa, 4 * M}, {"sb", sb, 4 * N}});
         on_current_device(a, "a");
         if (M == 0 || N == 0) return NVFP4_OK;
         return entries.int8_gemm(static_cast<int8_t*>(a.data_ptr()), static_cast<float*>(sa),
@@ -249,13 +295,14 @@ PyObject* py_nvfp4_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
         const at::Tensor& a = *tensor(v[0], "a");
         const int64_t prepared = integer(v[4], "prepared");
         void* pa = need_bytes(&a, "a", M * (K / 2), a);
-        void* sfa = need_bytes(tensor(v[1], "sfa"), "sfa", (int64_t)entries.scale_bytes(M, K), a);
+        const int64_t sfa_bytes = (int64_t)entries.scale_bytes(M, K);
+        void* sfa = need_bytes(tensor(v[1], "sfa"), "sfa", sfa_bytes, a);
         void* b = need_bytes(tensor(v[2], "b"), "b", N * (K / 2), a);
-        void* sfb = need_bytes(tensor(v[3], "sfb"), "sfb",
-                               (int64_t)(prepared ? entries.prepared_bytes(N, K) : entries.scale_bytes(N, K)), a);
-        void* alpha = need(tensor(v[5], "alpha"), "alpha", at::kFloat, {1}, a);
+        const int64_t sfb_bytes = (int64_t)(prepared ? entries.prepared_bytes(N, K) : entries.scale_bytes(N, K));
+        void* sfb = need_bytes(tensor(v[3], "sfb"), "sfb", sfb_bytes, a);
+        void* alpha = need_scalar(tensor(v[5], "alpha"), "alpha", a);
         const EpilogueArgs e = epilogue_args(v[6], v[7], v[8], v[9], M, N, a);
-        not_over(e, M, N, pa, M * (K / 2), "a");
+        not_over(e, M, N, {{"a", pa, M * (K / 2)}, {"b", b, N * (K / 2)}, {"sfa", sfa, sfa_bytes}, {"sfb", sfb, sfb_bytes}});
         on_current_device(a, "a");
         if (M == 0 || N == 0) return NVFP4_OK;
         return entries.nvfp4_gemm(static_cast<uint8_t*>(pa), static_cast<uint8_t*>(sfa),
@@ -276,6 +323,8 @@ PyObject* py_int8_linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
         const EpilogueArgs e = epilogue_args(v[3], v[4], v[5], v[7], M, N, x);
         const at::Tensor* ws = tensor(v[6], "workspace");
         void* pws = need_bytes(ws, "workspace", 0, x);
+        not_over(e, M, N, {{"wq", wq, N * K}, {"sw", sw, 4 * N}, {"workspace", pws, ws->numel()}});
+        workspace_apart(e, M, N, x, *ws);
         on_current_device(x, "x");
         if (M == 0 || N == 0) return NVFP4_OK;
         return entries.int8_linear(x.data_ptr(), M, K, static_cast<int8_t*>(wq), static_cast<float*>(sw), N,
@@ -293,13 +342,15 @@ PyObject* py_nvfp4_linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
         if (N < 0) return NVFP4_ERR_INVALID_ARG;
         const int64_t prepared = integer(v[3], "prepared");
         void* w = need_bytes(tensor(v[1], "w_packed"), "w_packed", N * (K / 2), x);
-        void* sf = need_bytes(tensor(v[2], "w_sf"), "w_sf",
-                              (int64_t)(prepared ? entries.prepared_bytes(N, K) : entries.scale_bytes(N, K)), x);
-        void* gsf_w = need(tensor(v[4], "gsf_w"), "gsf_w", at::kFloat, {1}, x);
-        void* gsf_x = need(tensor(v[7], "gsf_x", true), "gsf_x", at::kFloat, {1}, x);
+        const int64_t sf_bytes = (int64_t)(prepared ? entries.prepared_bytes(N, K) : entries.scale_bytes(N, K));
+        void* sf = need_bytes(tensor(v[2], "w_sf"), "w_sf", sf_bytes, x);
+        void* gsf_w = need_scalar(tensor(v[4], "gsf_w"), "gsf_w", x);
+        void* gsf_x = need_scalar(tensor(v[7], "gsf_x", true), "gsf_x", x);
         const EpilogueArgs e = epilogue_args(v[6], v[9], v[10], v[12], M, N, x);
         const at::Tensor* ws = tensor(v[11], "workspace");
         void* pws = need_bytes(ws, "workspace", 0, x);
+        not_over(e, M, N, {{"w_packed", w, N * (K / 2)}, {"w_sf", sf, sf_bytes}, {"workspace", pws, ws->numel()}});
+        workspace_apart(e, M, N, x, *ws);
         const int group = (int)integer(v[8], "rotate_group");
         on_current_device(x, "x");
         if (M == 0 || N == 0) return NVFP4_OK;

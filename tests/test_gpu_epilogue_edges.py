@@ -45,3 +45,39 @@ def test_nan_scales_stay_in_their_row_and_column(M, N, K, prepared):
     bad[bad_m, :] = True
     assert torch.isnan(y[bad]).all()
     assert torch.equal(y[~bad].view(torch.int16), clean[~bad].view(torch.int16))
+
+
+@pytest.mark.parametrize("kind", ["int8", "nvfp4"])
+@pytest.mark.parametrize("M,K", [(1, 1024), (40, 512), (300, 576), (2500, 1088)])
+def test_linear_onto_its_own_input(kind, M, K):
+    """out is x, and the residual too: x is read, then written."""
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    x = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+    w = (torch.randn(K, K, generator=g, device="cuda") * K ** -0.5).to(torch.bfloat16)
+    if kind == "int8":
+        def call(x, **kw):
+            return nv.int8_linear_act(x, *nv.int8_quantize_rows(w), activation="gelu", **kw)
+    else:
+        def call(x, **kw):
+            return nv.nvfp4_linear_act(x, *nv.pack_weight(w), K, activation="gelu", **kw)
+    want = call(x, residual=x)
+    for _ in range(5):
+        live = x.clone()
+        call(live, residual=live, out=live)
+        torch.cuda.synchronize()
+        assert nv.last_device_status() == nv.OK
+        assert torch.equal(live.view(torch.int16), want.view(torch.int16))
+
+
+def test_scalars_without_dimensions():
+    M, N, K = 4, 64, 128
+    a, sfa, b, sfb, alpha = operands("nvfp4", M, N, K)
+    want = nv.nvfp4_gemm_act(a, sfa, b, sfb, alpha.reshape(1), None, M, N, K)
+    got = nv.nvfp4_gemm_act(a, sfa, b, sfb, alpha.reshape(()), None, M, N, K)
+    x = torch.randn(M, K, device="cuda").to(torch.bfloat16)
+    gsf = torch.tensor(30.0, device="cuda")
+    one = nv.nvfp4_rmsnorm_quantize(x, None, gsf, 1e-6)
+    two = nv.nvfp4_rmsnorm_quantize(x, None, gsf.reshape(1), 1e-6)
+    torch.cuda.synchronize()
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+    assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
