@@ -81,7 +81,6 @@ struct PairParams {
     int k_tiles;               // stages of K
     int kchunks;               // 32-byte K steps
     int prepared;              // B scales: 1 = prepared blocks, 0 = 128x4 chunks
-    int tma_store;             // n_out % 8 == 0
     int w_early;               // B was complete before the previous kernel started
     int* status;
     uint64_t budget_ns;
@@ -234,16 +233,20 @@ __device__ __forceinline__ Item pair_item(const PairParams& p, int item) {
     return {m_blk, n_blk * PN + (half ? ((item - p.whole) & 1) * (PN / 2) : 0), half};
 }
 
-// RES: a residual that TMA can load (n_out % 8 == 0).  A build of its own: tested per value
-// instead, its predicated-off loads, unpacking and additions were a quarter of the
-// instructions of a call without one.
-template <bool I8, int ACT, bool GATED, bool RES>
+// How a tile leaves: by TMA without a residual, by TMA with one (both n_out % 8 == 0), or, with
+// rows that are not 16-byte multiples, by the lanes (RAGGED).  Each a build of its own: a
+// residual tested per value was a quarter of the instructions of a call without one, and the
+// lanes' code beside the TMA form cost that its registers (FFN-in with GELU 111 -> 116 us).
+enum { OUT_PLAIN, OUT_RES, OUT_RAGGED };
+
+template <bool I8, int ACT, bool GATED, int OUT>
 __global__ void __launch_bounds__(PTHREADS, 1)
 gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmSFA,
                  const __grid_constant__ CUtensorMap tmSFB, const __grid_constant__ CUtensorMap tmY,
                  const __grid_constant__ CUtensorMap tmR, const PairParams p) {
     using SM = PairSmem<I8>;
+    constexpr bool RES = OUT == OUT_RES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -582,7 +585,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         columns8(c, o, u);
                     }
                 };
-                if (p.tma_store) {
+                if constexpr (OUT != OUT_RAGGED) {
                     bool stored = false;
 #pragma unroll
                     for (int c = 0; c < (GATED ? 1 : 2); ++c) {
@@ -637,25 +640,79 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         else load_residual(next_row, next_n0 + 64 * part0);
                     }
                 } else {
-                    // rows of y are not 16-byte multiples: element by element
-                    const int row = row0 + lane;
+                    // Rows of y are not 16-byte multiples, so TMA cannot store them.  The values of
+                    // a chunk go through the staging tiles in fp32 (4 KiB), where 16-byte piece o
+                    // of row r sits at o ^ (r & 7), and leave in rows of neighbouring columns:
+                    // straight from the accumulator each lane would write its own row, 32 sectors
+                    // an instruction, with the residual's loads held up by the stores before
+                    // them (the residual may be y).  8538 x 6230 x 3584 FP4 537 -> 107 us (6232
+                    // columns: 93), with a residual 839 -> 126; 531 x 8982 x 416 int8 104 -> 18.5
+                    // (8984: 13.6), 8981 columns 105 -> 35.
+                    const int rows = min(32, p.M - row0);
 #pragma unroll
-                    for (int c = 0; c < (GATED ? 1 : 2); ++c)
+                    for (int c = 0; c < (GATED ? 1 : 2); ++c) {
+                        const int col = GATED ? n0 >> 1 : n0 + 32 * c;
+                        if (col >= p.n_out || rows <= 0) continue;    // warp-uniform
+                        __syncwarp();                                 // the last chunk has been read
 #pragma unroll
                         for (int o = 0; o < 4; ++o) {
                             float u[8];
                             outputs8(c, o, u);
-                            const int col = (GATED ? n0 >> 1 : n0 + 32 * c) + 8 * o;
-                            if (row >= p.M) continue;
-                            const size_t to = (size_t)row * p.n_out + col;
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (col + j < p.n_out) {
-                                    if (p.residual)
-                                        u[j] = __fadd_rn(u[j], __uint_as_float((uint32_t)p.residual[to + j] << 16));
-                                    p.y[to + j] = (uint16_t)bf16x2_rn(u[j], 0.0f);
-                                }
+                            for (int q = 0; q < 2; ++q)
+                                *reinterpret_cast<float4*>(stg + lane * 128 + (((2 * o + q) ^ (lane & 7)) << 4)) =
+                                    make_float4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
                         }
+                        __syncwarp();
+                        const size_t to0 = (size_t)row0 * p.n_out + col;
+                        const uint16_t* res = p.residual;
+                        if (p.n_out & 1) {
+                            // one value a lane, a row at a time; eight rows' loads in flight (with
+                            // sixteen 8538 x 6229 x 3584 takes 175 us, with eight 113)
+                            const bool mine = col + lane < p.n_out;
+#pragma unroll 1
+                            for (int r8 = 0; r8 < rows; r8 += 8) {
+                                uint32_t t[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    t[k] = res && mine && r8 + k < rows
+                                               ? res[to0 + (size_t)(r8 + k) * p.n_out + lane] : 0u;
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    float u = *reinterpret_cast<const float*>(
+                                        stg + (r8 + k) * 128 + (((lane >> 2) ^ k) << 4) + (lane & 3) * 4);
+                                    if (res) u = __fadd_rn(u, bf16lo(t[k]));
+                                    if (mine && r8 + k < rows)
+                                        p.y[to0 + (size_t)(r8 + k) * p.n_out + lane] = (uint16_t)bf16x2_rn(u, 0.0f);
+                                }
+                            }
+                        } else {
+                            // two values a lane, two rows at a time, all loads in flight (of four
+                            // steps' at a time: 531 x 8982 x 416 23.6 us)
+                            const int cl = 2 * (lane & 15), rl = lane >> 4;
+                            const bool mine = col + cl < p.n_out;
+                            uint32_t t[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                t[k] = res && mine && 2 * k + rl < rows
+                                           ? *reinterpret_cast<const uint32_t*>(
+                                                 res + to0 + (size_t)(2 * k + rl) * p.n_out + cl)
+                                           : 0u;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const int r = 2 * k + rl;
+                                float2 u = *reinterpret_cast<const float2*>(
+                                    stg + r * 128 + (((cl >> 2) ^ (r & 7)) << 4) + (cl & 3) * 4);
+                                if (res) {
+                                    u.x = __fadd_rn(u.x, bf16lo(t[k]));
+                                    u.y = __fadd_rn(u.y, bf16hi(t[k]));
+                                }
+                                if (mine && r < rows)
+                                    *reinterpret_cast<uint32_t*>(p.y + to0 + (size_t)r * p.n_out + cl) =
+                                        bf16x2_rn(u.x, u.y);
+                            }
+                        }
+                    }
                 }
             }
         }
@@ -700,22 +757,28 @@ namespace {
 using PairKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
                             CUtensorMap, CUtensorMap, PairParams);
 
-template <bool I8, bool GATED, bool RES>
+template <bool I8, bool GATED, int OUT>
 PairKernel pair_kernel_of(int base) {
-    static const PairKernel table[5] = {gemm_pair_kernel<I8, NVFP4_ACT_NONE, GATED, RES>,
-                                        gemm_pair_kernel<I8, NVFP4_ACT_RELU, GATED, RES>,
-                                        gemm_pair_kernel<I8, NVFP4_ACT_GELU, GATED, RES>,
-                                        gemm_pair_kernel<I8, NVFP4_ACT_GELU_TANH, GATED, RES>,
-                                        gemm_pair_kernel<I8, NVFP4_ACT_SILU, GATED, RES>};
+    static const PairKernel table[5] = {gemm_pair_kernel<I8, NVFP4_ACT_NONE, GATED, OUT>,
+                                        gemm_pair_kernel<I8, NVFP4_ACT_RELU, GATED, OUT>,
+                                        gemm_pair_kernel<I8, NVFP4_ACT_GELU, GATED, OUT>,
+                                        gemm_pair_kernel<I8, NVFP4_ACT_GELU_TANH, GATED, OUT>,
+                                        gemm_pair_kernel<I8, NVFP4_ACT_SILU, GATED, OUT>};
     return table[base];
 }
 
+template <bool I8, bool GATED>
+PairKernel pair_kernel_of(int base, int out) {
+    if (out == OUT_RES) return pair_kernel_of<I8, GATED, OUT_RES>(base);
+    if (out == OUT_RAGGED) return pair_kernel_of<I8, GATED, OUT_RAGGED>(base);
+    return pair_kernel_of<I8, GATED, OUT_PLAIN>(base);
+}
+
 template <bool I8>
-PairKernel pair_kernel(int activation, bool res) {
+PairKernel pair_kernel(int activation, int out) {
     const int base = activation & ~NVFP4_ACT_GATED;
-    if (activation & NVFP4_ACT_GATED)
-        return res ? pair_kernel_of<I8, true, true>(base) : pair_kernel_of<I8, true, false>(base);
-    return res ? pair_kernel_of<I8, false, true>(base) : pair_kernel_of<I8, false, false>(base);
+    return activation & NVFP4_ACT_GATED ? pair_kernel_of<I8, true>(base, out)
+                                        : pair_kernel_of<I8, false>(base, out);
 }
 
 template <bool I8>
@@ -747,14 +810,13 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
     p.k_tiles = (int)((kbytes + PKB - 1) / PKB);
     p.kchunks = (int)(kbytes / 32);
     p.prepared = g.sfb_prepared ? 1 : 0;
-    p.tma_store = p.n_out % 8 == 0;
     p.w_early = g.weights_ready ? 1 : 0;
     p.status = status;
     p.budget_ns = 4000000000ull;   // 4 s
-    const bool res = p.residual && p.tma_store;
-    const PairKernel kernel = pair_kernel<I8>(g.epi.activation, res);
-    static std::atomic<int> attr_set[64][2][32];
-    std::atomic<int>& set = attr_set[dev.device & 63][res][g.epi.activation & 31];
+    const int out = p.n_out % 8 ? OUT_RAGGED : p.residual ? OUT_RES : OUT_PLAIN;
+    const PairKernel kernel = pair_kernel<I8>(g.epi.activation, out);
+    static std::atomic<int> attr_set[64][3][32];
+    std::atomic<int>& set = attr_set[dev.device & 63][out][g.epi.activation & 31];
     if (!set.load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  PairSmem<I8>::BYTES) != cudaSuccess)
@@ -773,9 +835,9 @@ nvfp4_status launch_pair_impl(const GemmActArgs& g, cudaStream_t stream) {
                          : make_scale_map(&mapSFB, g.sfb, p.kchunks, (g.N + 127) / 128)))
             return NVFP4_ERR_CUDA;
     }
-    if (p.tma_store && !make_output_map(&mapY, g.y, g.M, p.n_out)) return NVFP4_ERR_CUDA;
+    if (out != OUT_RAGGED && !make_output_map(&mapY, g.y, g.M, p.n_out)) return NVFP4_ERR_CUDA;
     mapR = mapY;
-    if (res && !make_output_map(&mapR, const_cast<void*>(g.epi.residual), g.M, p.n_out))
+    if (out == OUT_RES && !make_output_map(&mapR, const_cast<void*>(g.epi.residual), g.M, p.n_out))
         return NVFP4_ERR_CUDA;
 
     const int pairs = p.items < max_pairs ? p.items : max_pairs;

@@ -3,7 +3,8 @@ import pytest
 import torch
 
 import nvfp4_block_scaled_17_b200 as nv
-from test_gpu_epilogue import extras, operands, run
+import plain_ops as P
+from test_gpu_epilogue import extras, operands, product, run
 
 pytestmark = pytest.mark.gpu
 NAN_SCALE = 0x7F
@@ -81,3 +82,30 @@ def test_scalars_without_dimensions():
     torch.cuda.synchronize()
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
     assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+
+
+@pytest.mark.parametrize("kind", ["int8", "nvfp4"])
+@pytest.mark.parametrize("M,N", [(2500, 2062), (2500, 2061), (2499, 2060), (300, 522), (301, 521),
+                                 (129, 2598), (8200, 1033)])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_widths_that_tma_cannot_store(kind, M, N, gated, in_place):
+    """The columns and rows around y stay as they were, with and without a residual."""
+    K, cols = 192, N // 2 if gated else N
+    if gated and N % 2:
+        N, cols = N + 1, (N + 1) // 2
+    ops = operands(kind, M, N, K)
+    bias, res = extras(M, N, gated, True, True)
+    pad = 64
+    whole = torch.full((pad + M * cols + pad,), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = whole[pad:pad + M * cols].view(M, cols)
+    for r in (res, None):
+        if in_place and r is not None:
+            y.copy_(r)
+        run(kind, ops, M, N, K, bias, "silu", gated, y if in_place and r is not None else r, out=y)
+        torch.cuda.synchronize()
+        assert nv.last_device_status() == nv.OK
+        assert (whole[:pad] == 7.0).all() and (whole[pad + M * cols:] == 7.0).all()
+        v, dv = product(kind, ops, M, N, K, bias)
+        y64, bound = P.epilogue_64(v, dv, "silu", gated, r)
+        P.check(y, y64, bound, f"{kind} {M}x{N} gated={gated} residual={r is not None}")
