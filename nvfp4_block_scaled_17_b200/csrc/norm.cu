@@ -6,7 +6,7 @@
 //     n = bf16(fp32(fp32(h * rstd) * w))
 // followed by the library's own encoding of n: per-row int8 codes (int8_quantize_rows) or
 // NVFP4 codes under a static global scale (nvfp4_quantize without rotation).  The codes
-// equal those of the separate passes on the bf16 n bit for bit.
+// equal those of the separate passes on the bf16 n bit for bit, NaN and infinities included.
 //
 // The sum of squares is kept in 64 bits: the square of a bf16 value is exact there and the
 // sum's relative error is below 2^-49 for any row, so rstd (one rounding to fp32) does not
@@ -17,8 +17,9 @@
 // into registers and every store is 16 bytes wide (8 for FP4 codes).
 //
 // Bound by HBM: with a residual 7 bytes a value (int8; 6.56 FP4), each moved once.  B200,
-// graph replay: 32768 x 5120 int8 196 us, 6.00 TB/s (0.92 of the measured copy rate; 215
-// before the arithmetic was packed in pairs and the codes were rounded by an addition);
+// graph replay: 32768 x 5120 int8 193 us, 6.08 TB/s (0.93 of the measured copy rate; 215
+// before the arithmetic was packed in pairs and the codes were rounded by an addition, 199
+// with a minimum per value that gives a NaN's code, where one branch per row takes 193);
 // 32768 x 1024 FP4 37.5 us, 5.87 TB/s (0.90); a single row of 5120 2.7 us, of which a launch
 // alone takes two.  Fetching the next row while the current one is worked on gained nothing:
 // six blocks of 320 threads on an SM cover the latency already.
@@ -26,6 +27,7 @@
 #include "kernels.h"
 
 #include <atomic>
+#include <type_traits>
 
 namespace nvfp4 {
 
@@ -71,44 +73,79 @@ __device__ __forceinline__ void store_unit(uint16_t* p, const Unit& u) {
     *reinterpret_cast<uint4*>(p + 8) = make_uint4(u.w[4], u.w[5], u.w[6], u.w[7]);
 }
 
+// As absmax2_bf16, but a NaN in either operand stays.
+__device__ __forceinline__ uint32_t absmax2_nan_bf16(uint32_t a, uint32_t b) {
+    uint32_t m;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+}
+
+template <uint32_t (*MAX)(uint32_t, uint32_t)>
 __device__ __forceinline__ uint32_t unit_absmax(const Unit& u) {
-    return absmax2_bf16(absmax2_bf16(absmax2_bf16(u.w[0], u.w[1]), absmax2_bf16(u.w[2], u.w[3])),
-                        absmax2_bf16(absmax2_bf16(u.w[4], u.w[5]), absmax2_bf16(u.w[6], u.w[7])));
+    return MAX(MAX(MAX(u.w[0], u.w[1]), MAX(u.w[2], u.w[3])),
+               MAX(MAX(u.w[4], u.w[5]), MAX(u.w[6], u.w[7])));
+}
+
+// The maximum over a row's units: of the lane's (h), the warp's, and with BLOCK the block's.
+// red holds a value for each warp.
+template <uint32_t (*MAX)(uint32_t, uint32_t), int C, bool BLOCK>
+__device__ __forceinline__ uint32_t row_absmax(const Unit (&h)[C], uint32_t* red, int warps) {
+    const int lane = threadIdx.x & 31;
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < C; ++i) m = MAX(m, unit_absmax<MAX>(h[i]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = MAX(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if constexpr (BLOCK) {
+        if (lane == 0) red[threadIdx.x >> 5] = m;
+        __syncthreads();
+        m = lane < warps ? red[lane] : 0u;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = MAX(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    return m;
 }
 
 __device__ __forceinline__ float2 pair_of(uint32_t w) { return make_float2(bf16lo(w), bf16hi(w)); }
 __device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
 
-// 16 int8 codes of a unit under the row scale s; r = rn(1 / s).  rn(n / s) by one
-// remainder step (Markstein), as int8_quantize_rows computes it; a subnormal s, whose
-// reciprocal would overflow, takes the division, and s = 0 gives zeros.  Adding 1.5 * 2^23
-// rounds |t| <= 127 to a whole number, half to even, whose low byte is the code.
-__device__ __forceinline__ uint4 int8_codes(const Unit& u, float s, float r, bool fast) {
+// 16 int8 codes of a unit under the row scale s; r = rn(1 / s).  fast: rn(n / s) by one
+// remainder step (Markstein), as int8_quantize_rows computes it, and a whole number by adding
+// 1.5 * 2^23, which rounds |t| <= 127 half to even and leaves the code in the low byte.
+// Otherwise, for a subnormal s (its reciprocal would overflow; s = 0 gives zeros) and for rows
+// with a NaN or an infinity, a division and a conversion, in which a NaN gives 0.
+// 16 int8 codes of a unit under the row scale s; r = rn(1 / s).  FAST: rn(n / s) by one
+// remainder step (Markstein), as int8_quantize_rows computes it, and a whole number by adding
+// 1.5 * 2^23, which rounds |t| <= 127 half to even and leaves the code in the low byte.
+// Otherwise, for a subnormal s (its reciprocal would overflow; s = 0 gives zeros) and for rows
+// with a NaN or an infinity, a division and a conversion, in which a NaN gives 0.
+template <bool FAST>
+__device__ __forceinline__ uint4 int8_codes(const Unit& u, float s, float r) {
     uint32_t out[4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-        float2 c[2];
+        uint32_t c[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float2 v = pair_of(u.w[2 * g + j]);
-            float2 t;
-            if (fast) {
+            if constexpr (FAST) {
                 const float2 q0 = __fmul2_rn(v, twice(r));
-                t = __ffma2_rn(__ffma2_rn(q0, twice(-s), v), twice(r), q0);
+                const float2 t = __ffma2_rn(__ffma2_rn(q0, twice(-s), v), twice(r), q0);
+                c[2 * j] = __float_as_uint(__fadd_rn(t.x, 12582912.0f));
+                c[2 * j + 1] = __float_as_uint(__fadd_rn(t.y, 12582912.0f));
             } else {
-                t = s != 0.0f ? make_float2(__fdiv_rn(v.x, s), __fdiv_rn(v.y, s)) : twice(0.0f);
+                c[2 * j] = s != 0.0f ? (uint32_t)__float2int_rn(__fdiv_rn(v.x, s)) : 0u;
+                c[2 * j + 1] = s != 0.0f ? (uint32_t)__float2int_rn(__fdiv_rn(v.y, s)) : 0u;
             }
-            c[j] = make_float2(__fadd_rn(t.x, 12582912.0f), __fadd_rn(t.y, 12582912.0f));
         }
-        out[g] = __byte_perm(__byte_perm(__float_as_uint(c[0].x), __float_as_uint(c[0].y), 0x0040),
-                             __byte_perm(__float_as_uint(c[1].x), __float_as_uint(c[1].y), 0x0040), 0x5410);
+        out[g] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
     }
     return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 // One block of 16 values as nvfp4_quantize encodes it under a static global scale.
 __device__ __forceinline__ uint32_t fp4_codes(const Unit& u, float gsf, uint2& codes) {
-    const uint32_t s8 = e4m3_scale_of_scaled_max(__fmul_rn(gsf, absmax_of_pair(unit_absmax(u))));
+    const uint32_t s8 = e4m3_scale_of_scaled_max(__fmul_rn(gsf, absmax_of_pair(unit_absmax<absmax2_bf16>(u))));
     const float inv = (s8 == 0u || s8 == 127u) ? 0.0f : __fdiv_rn(gsf, f32_from_e4m3(s8));
     float v[2][8];
 #pragma unroll
@@ -194,7 +231,6 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : kNormWarpThreads) norm_kernel(c
         }
         const float rstd = (float)rsqrt(ss * p.inv_k + p.eps);
 
-        uint32_t m = 0u;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int u = i * span + tid;
@@ -207,7 +243,6 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : kNormWarpThreads) norm_kernel(c
                 h[i].w[j] = bf16x2_rn(t.x, t.y);
             }
             if (p.n_out && u < p.units) store_unit(p.n_out + row * p.K + 16 * (int64_t)u, h[i]);
-            if constexpr (!FP4) m = absmax2_bf16(m, unit_absmax(h[i]));
         }
         if constexpr (FP4) {
 #pragma unroll
@@ -224,27 +259,28 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : kNormWarpThreads) norm_kernel(c
                          (((row >> 5) & 3) << 2) + (u & 3)] = (uint8_t)s8;
             }
         } else {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = absmax2_bf16(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if constexpr (BLOCK) {
-                if (lane == 0) red_mx[warp] = m;
-                __syncthreads();
-                m = lane < warps ? red_mx[lane] : 0u;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    m = absmax2_bf16(m, __shfl_xor_sync(0xffffffffu, m, o));
+            // The scale comes from the values that are no NaN, as int8_quantize_rows takes it: a
+            // second reduction in the rows that have one (the row's threads agree).
+            uint32_t m = row_absmax<absmax2_nan_bf16, C, BLOCK>(h, red_mx, warps);
+            const bool finite = (m & 0x7fffu) < 0x7f80u && (m & 0x7fff0000u) < 0x7f800000u;
+            if (!finite) {
+                if (BLOCK) __syncthreads();            // red_mx has been read
+                m = row_absmax<absmax2_bf16, C, BLOCK>(h, red_mx, warps);
             }
             const float s = __fdiv_rn(absmax_of_pair(m), 127.0f);
             if (tid == 0) p.scale[row] = s;
-            const bool fast = s >= 1.17549435e-38f;
-            const float r = fast ? __frcp_rn(s) : 0.0f;
+            const bool fast = finite && s >= 1.17549435e-38f;
+            auto store = [&](auto form, float r) {
 #pragma unroll
-            for (int i = 0; i < C; ++i) {
-                const int u = i * span + tid;
-                if (u < p.units)
-                    *reinterpret_cast<uint4*>(p.q + row * p.K + 16 * (int64_t)u) =
-                        int8_codes(h[i], s, r, fast);
-            }
+                for (int i = 0; i < C; ++i) {
+                    const int u = i * span + tid;
+                    if (u < p.units)
+                        *reinterpret_cast<uint4*>(p.q + row * p.K + 16 * (int64_t)u) =
+                            int8_codes<decltype(form)::value>(h[i], s, r);
+                }
+            };
+            if (fast) store(std::true_type{}, __frcp_rn(s));
+            else store(std::false_type{}, 0.0f);
         }
         if constexpr (FP4 && BLOCK) __syncthreads();   // red_ss is free for the next row
     }
