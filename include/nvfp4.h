@@ -378,7 +378,7 @@ NVFP4_API nvfp4_status nvfp4_rmsnorm_quantize(const void* x_bf16, const void* re
  *     u[m, j] = act(v[m, 2j]) * v[m, 2j + 1]       gated: n_out = N / 2 columns
  *     y[m, j] = bf16(u[m, j] + residual[m, j])
  * in fp32 with the one rounding at the end.  The activations are within 5e-7 * max(|v|, 1)
- * of their 64-bit values before that rounding.
+ * of their 64-bit values before that rounding; far to the left the last three are 0.
  *   activation    : NVFP4_ACT_*; gated: the weight's rows 2j and 2j + 1 hold the gate's and
  *                   the up projection's row j (bias likewise), N even
  *   residual_bf16 : in,  bf16 [M, n_out] or NULL; may equal y (in place), otherwise may not
