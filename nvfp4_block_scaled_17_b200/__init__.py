@@ -8,6 +8,10 @@ that library's CUDA kernels.  PyTorch only provides device memory and the curren
 stream.  There is no CPU fallback: if the library is missing or the device is not
 a B200, the calls raise.  Most calls are marshalled by ctypes; those of the norms and of the
 products with an epilogue, which serve single tokens, by a small extension module.
+
+A call runs on the current stream, or on the one given as ``stream``; what it allocates then
+belongs to that stream, as under ``torch.cuda.stream(stream)``.  The tensors it is given, and
+when their producers and consumers run, stay the caller's matter.
 """
 from __future__ import annotations
 
@@ -141,11 +145,37 @@ def _bf16_2d(x: torch.Tensor, name: str) -> torch.Tensor:
     return x
 
 
-def _scalar(t, device, name):
+def _empty(stream, dtype, device, *shape):
+    """An output of a call on this stream (None: the current one), of the stream's own memory.
+
+    A block of the current stream's would not do for a call on another: it may still be in use
+    there, and, freed, be handed out there while the call runs.  The caller may use an output on
+    the current stream all the same, so freeing it waits for that.  (The shape in separate
+    arguments: torch.empty takes 0.9 us longer over a tuple.)"""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(*shape, dtype=dtype, device=device)
+    if t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _workspace(n: int, device, stream, dtype=torch.uint8):
+    """Memory that only the call uses: n bytes (or values), of its stream's own."""
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=device)
+
+
+def _scalar(t, device, name, stream=None):
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
-        t = torch.tensor(float(t), dtype=torch.float32, device=device)
+        v, t = float(t), _workspace(1, device, stream, torch.float32)
+        with torch.cuda.stream(stream):          # None: no change
+            t.fill_(v)
     if t.dtype != torch.float32 or t.numel() != 1 or not t.is_cuda:
         raise TypeError(f"{name} must be a one-element CUDA float32 tensor")
     return t
@@ -179,7 +209,7 @@ def hadamard_rotate(x: torch.Tensor, group: int, out: torch.Tensor | None = None
                     stream=None) -> torch.Tensor:
     """bf16 [rows, K] -> bf16 [rows, K], each group of `group` values times H/sqrt(g)."""
     _bf16_2d(x, "x")
-    y = torch.empty_like(x) if out is None else out
+    y = _empty(stream, x.dtype, x.device, *x.shape) if out is None else out
     _check("hadamard_rotate", lib().hadamard_rotate(_ptr(x), _ptr(y), x.shape[0], x.shape[1],
                                                     int(group), _stream(stream)))
     return y
@@ -195,16 +225,16 @@ def nvfp4_quantize(x: torch.Tensor, rotate_group: int = 0, gsf: torch.Tensor | f
     gsf_w and alpha_out the kernel also writes alpha = 1/(gsf * gsf_w) for nvfp4_gemm."""
     _bf16_2d(x, "x")
     R, K = x.shape
-    gsf_in = _scalar(gsf, x.device, "gsf")
+    gsf_in = _scalar(gsf, x.device, "gsf", stream)
     if out is None:
-        packed = torch.empty(R, K // 2, dtype=torch.uint8, device=x.device)
-        sf = torch.empty(max(nvfp4_scale_bytes(R, K), 1), dtype=torch.uint8, device=x.device)
-        gsf_out = torch.empty(1, dtype=torch.float32, device=x.device)
+        packed = _empty(stream, torch.uint8, x.device, R, K // 2)
+        sf = _empty(stream, torch.uint8, x.device, max(nvfp4_scale_bytes(R, K), 1))
+        gsf_out = _empty(stream, torch.float32, x.device, 1)
     else:
         packed, sf, gsf_out = out
     ws = workspace
     if gsf_in is None and ws is None:
-        ws = torch.empty(nvfp4_quantize_workspace_bytes(), dtype=torch.uint8, device=x.device)
+        ws = _workspace(nvfp4_quantize_workspace_bytes(), x.device, stream)
     _check("nvfp4_quantize", lib().nvfp4_quantize(
         _ptr(x), R, K, int(rotate_group), _ptr(gsf_in), _ptr(gsf_out), _ptr(packed), _ptr(sf),
         _ptr(gsf_w), _ptr(alpha_out), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
@@ -215,8 +245,8 @@ def nvfp4_gemm(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: torch.T
                alpha: torch.Tensor, bias: torch.Tensor | None, M: int, N: int, K: int,
                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y bf16 [M, N] = bf16(alpha * deq(a) deq(b)^T + bias)."""
-    alpha = _scalar(alpha, a.device, "alpha")
-    y = torch.empty(M, N, dtype=torch.bfloat16, device=a.device) if out is None else out
+    alpha = _scalar(alpha, a.device, "alpha", stream)
+    y = _empty(stream, torch.bfloat16, a.device, M, N) if out is None else out
     _check("nvfp4_gemm", lib().nvfp4_gemm(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(alpha),
                                           _ptr(bias), _ptr(y), M, N, K, _stream(stream)))
     return y
@@ -228,8 +258,8 @@ def nvfp4_debug_gemm_f32(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sf
                          stream=None) -> torch.Tensor:
     """The GEMM with its unrounded output: y fp32 [M, N] = fp32(alpha * acc) + bias (the
     value nvfp4_gemm / nvfp4_gemm_prepared round once to bf16)."""
-    alpha = _scalar(alpha, a.device, "alpha")
-    y = torch.empty(M, N, dtype=torch.float32, device=a.device) if out is None else out
+    alpha = _scalar(alpha, a.device, "alpha", stream)
+    y = _empty(stream, torch.float32, a.device, M, N) if out is None else out
     _check("nvfp4_debug_gemm_f32", lib().nvfp4_debug_gemm_f32(
         _ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), 1 if prepared else 0, _ptr(alpha), _ptr(bias),
         _ptr(y), M, N, K, _stream(stream)))
@@ -245,8 +275,7 @@ def prepare_weight_scales(sf: torch.Tensor, N: int, K: int, out: torch.Tensor | 
     """A weight's 128x4 scales in the order nvfp4_gemm_prepared / nvfp4_linear_prepared
     read (one 4 KiB block per 256-row block and 256-value K stage)."""
     if out is None:
-        out = torch.empty(max(nvfp4_prepared_scale_bytes(N, K), 1), dtype=torch.uint8,
-                          device=sf.device)
+        out = _empty(stream, torch.uint8, sf.device, max(nvfp4_prepared_scale_bytes(N, K), 1))
     _check("nvfp4_prepare_weight_scales",
            lib().nvfp4_prepare_weight_scales(_ptr(sf), N, K, _ptr(out), _stream(stream)))
     return out
@@ -257,8 +286,8 @@ def nvfp4_gemm_prepared(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor,
                         bias: torch.Tensor | None, M: int, N: int, K: int,
                         out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """nvfp4_gemm with the weight scales from prepare_weight_scales."""
-    alpha = _scalar(alpha, a.device, "alpha")
-    y = torch.empty(M, N, dtype=torch.bfloat16, device=a.device) if out is None else out
+    alpha = _scalar(alpha, a.device, "alpha", stream)
+    y = _empty(stream, torch.bfloat16, a.device, M, N) if out is None else out
     _check("nvfp4_gemm_prepared", lib().nvfp4_gemm_prepared(
         _ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb_prepared), _ptr(alpha), _ptr(bias), _ptr(y), M, N,
         K, _stream(stream)))
@@ -274,12 +303,11 @@ def nvfp4_linear(x: torch.Tensor, w_packed: torch.Tensor, w_sf: torch.Tensor,
     With prepared=True, w_sf is the output of prepare_weight_scales."""
     _bf16_2d(x, "x")
     M, K = x.shape
-    gsf_x = _scalar(gsf_x, x.device, "gsf_x")
-    gsf_w = _scalar(gsf_w, x.device, "gsf_w")
+    gsf_x = _scalar(gsf_x, x.device, "gsf_x", stream)
+    gsf_w = _scalar(gsf_w, x.device, "gsf_w", stream)
     if workspace is None:
-        workspace = torch.empty(nvfp4_linear_workspace_bytes(M, K), dtype=torch.uint8,
-                                device=x.device)
-    y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device) if out is None else out
+        workspace = _workspace(nvfp4_linear_workspace_bytes(M, K), x.device, stream)
+    y = _empty(stream, torch.bfloat16, x.device, M, N) if out is None else out
     name = "nvfp4_linear_prepared" if prepared else "nvfp4_linear"
     _check(name, getattr(lib(), name)(
         _ptr(x), M, K, _ptr(w_packed), _ptr(w_sf), _ptr(gsf_w), N, _ptr(bias), _ptr(gsf_x),
@@ -293,11 +321,11 @@ def nvfp4_gemm_quantize_out(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor,
                             out: tuple | None = None, stream=None):
     """GEMM with the next linear's NVFP4 input as output: (packed uint8 [M, N/2], 128x4
     scales) of bf16(alpha * A B^T + bias) under the static global scale gsf_out."""
-    alpha = _scalar(alpha, a.device, "alpha")
-    gsf_out = _scalar(gsf_out, a.device, "gsf_out")
+    alpha = _scalar(alpha, a.device, "alpha", stream)
+    gsf_out = _scalar(gsf_out, a.device, "gsf_out", stream)
     if out is None:
-        packed = torch.empty(M, N // 2, dtype=torch.uint8, device=a.device)
-        sf = torch.empty(max(nvfp4_scale_bytes(M, N), 1), dtype=torch.uint8, device=a.device)
+        packed = _empty(stream, torch.uint8, a.device, M, N // 2)
+        sf = _empty(stream, torch.uint8, a.device, max(nvfp4_scale_bytes(M, N), 1))
     else:
         packed, sf = out
     _check("nvfp4_gemm_quantize_out", lib().nvfp4_gemm_quantize_out(
@@ -315,8 +343,8 @@ def int8_quantize_rows(x: torch.Tensor, out: tuple | None = None, stream=None):
     _bf16_2d(x, "x")
     R, K = x.shape
     if out is None:
-        q = torch.empty(R, K, dtype=torch.int8, device=x.device)
-        s = torch.empty(max(R, 1), dtype=torch.float32, device=x.device)
+        q = _empty(stream, torch.int8, x.device, R, K)
+        s = _empty(stream, torch.float32, x.device, max(R, 1))
     else:
         q, s = out
     _check("int8_quantize_rows", lib().int8_quantize_rows(_ptr(x), R, K, _ptr(q), _ptr(s),
@@ -330,7 +358,7 @@ def int8_gemm(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tens
     """y bf16 [M, N] = bf16((fp32(a b^T) * sa[m]) * sb[n] + bias)."""
     M, K = a.shape
     N = b.shape[0]
-    y = torch.empty(M, N, dtype=torch.bfloat16, device=a.device) if out is None else out
+    y = _empty(stream, torch.bfloat16, a.device, M, N) if out is None else out
     _check("int8_gemm", lib().int8_gemm(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(bias), _ptr(y),
                                         M, N, K, _stream(stream)))
     return y
@@ -345,9 +373,9 @@ def int8_linear(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
     M, K = x.shape
     N = wq.shape[0]
     if workspace is None:
-        workspace = torch.empty(max(int(lib().int8_linear_workspace_bytes(M, K)), 1),
-                                dtype=torch.uint8, device=x.device)
-    y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device) if out is None else out
+        workspace = _workspace(max(int(lib().int8_linear_workspace_bytes(M, K)), 1), x.device,
+                               stream)
+    y = _empty(stream, torch.bfloat16, x.device, M, N) if out is None else out
     _check("int8_linear", lib().int8_linear(_ptr(x), M, K, _ptr(wq), _ptr(sw), N, _ptr(bias),
                                             _ptr(workspace), workspace.numel(), _ptr(y),
                                             _stream(stream)))
@@ -368,9 +396,9 @@ def int8_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None, eps: flo
     it is not given, or None without a residual.  residual_out may be x or residual itself.
     norm_out, when given, receives n."""
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(x)
-    q, s = out or (torch.empty(x.shape, dtype=torch.int8, device=x.device),
-                   torch.empty(x.shape[:1], dtype=torch.float32, device=x.device))
+        residual_out = _empty(stream, x.dtype, x.device, *x.shape)
+    q, s = out or (_empty(stream, torch.int8, x.device, *x.shape),
+                   _empty(stream, torch.float32, x.device, *x.shape[:1]))
     st = _calls().int8_rmsnorm_quantize(x, weight, eps, residual, q, s, residual_out, norm_out,
                                         None if stream is None else stream.cuda_stream)
     if st:
@@ -389,9 +417,9 @@ def nvfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None, gsf: to
     Returns (packed uint8 [rows, K/2], scales uint8 [scale_bytes], h).  With gsf_w and
     alpha_out the kernel also writes alpha = 1/(gsf * gsf_w)."""
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(x)
+        residual_out = _empty(stream, x.dtype, x.device, *x.shape)
     calls = _calls()
-    packed, sf = out or _packed_like(x)
+    packed, sf = out or _packed_like(x, stream)
     st = calls.nvfp4_rmsnorm_quantize(x, weight, eps, residual, gsf, packed, sf, gsf_w, alpha_out,
                                       residual_out, norm_out,
                                       None if stream is None else stream.cuda_stream)
@@ -400,12 +428,12 @@ def nvfp4_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor | None, gsf: to
     return packed, sf, residual_out
 
 
-def _packed_like(x: torch.Tensor):
+def _packed_like(x: torch.Tensor, stream):
     if x.dim() != 2:
         raise ValueError("x must be a contiguous 2-D tensor")
     R, K = x.shape
-    return (torch.empty(R, K // 2, dtype=torch.uint8, device=x.device),
-            torch.empty(nvfp4_scale_bytes(R, K), dtype=torch.uint8, device=x.device))
+    return (_empty(stream, torch.uint8, x.device, R, K // 2),
+            _empty(stream, torch.uint8, x.device, nvfp4_scale_bytes(R, K)))
 
 
 # ---------------------------------------------------------------------------
@@ -446,7 +474,7 @@ def nvfp4_gemm_act(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: tor
     act = _activation(activation, gated, N)
     y = out
     if y is None:
-        y = torch.empty(M, N // 2 if gated else N, dtype=torch.bfloat16, device=a.device)
+        y = _empty(stream, torch.bfloat16, a.device, M, N // 2 if gated else N)
     st = _calls().nvfp4_gemm_act(a, sfa, b, sfb, prepared, alpha, bias, act, residual, y, M, N, K,
                                  None if stream is None else stream.cuda_stream)
     if st:
@@ -464,7 +492,7 @@ def int8_gemm_act(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.
     act = _activation(activation, gated, N)
     y = out
     if y is None:
-        y = torch.empty(a.shape[0], N // 2 if gated else N, dtype=torch.bfloat16, device=a.device)
+        y = _empty(stream, torch.bfloat16, a.device, a.shape[0], N // 2 if gated else N)
     st = _calls().int8_gemm_act(a, sa, b, sb, bias, act, residual, y,
                                 None if stream is None else stream.cuda_stream)
     if st:
@@ -484,10 +512,9 @@ def nvfp4_linear_act(x: torch.Tensor, w_packed: torch.Tensor, w_sf: torch.Tensor
     M, K = x.shape
     y = out
     if y is None:
-        y = torch.empty(M, N // 2 if gated else N, dtype=torch.bfloat16, device=x.device)
+        y = _empty(stream, torch.bfloat16, x.device, M, N // 2 if gated else N)
     if workspace is None:
-        workspace = torch.empty(nvfp4_linear_workspace_bytes(M, K), dtype=torch.uint8,
-                                device=x.device)
+        workspace = _workspace(nvfp4_linear_workspace_bytes(M, K), x.device, stream)
     st = _calls().nvfp4_linear_act(x, w_packed, w_sf, prepared, gsf_w, N, bias, gsf_x,
                                    rotate_group, act, residual, workspace, y,
                                    None if stream is None else stream.cuda_stream)
@@ -507,10 +534,10 @@ def int8_linear_act(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
     M, K = x.shape
     y = out
     if y is None:
-        y = torch.empty(M, N // 2 if gated else N, dtype=torch.bfloat16, device=x.device)
+        y = _empty(stream, torch.bfloat16, x.device, M, N // 2 if gated else N)
     if workspace is None:
-        workspace = torch.empty(max(int(lib().int8_linear_workspace_bytes(M, K)), 1),
-                                dtype=torch.uint8, device=x.device)
+        workspace = _workspace(max(int(lib().int8_linear_workspace_bytes(M, K)), 1), x.device,
+                               stream)
     st = _calls().int8_linear_act(x, wq, sw, bias, act, residual, workspace, y,
                                   None if stream is None else stream.cuda_stream)
     if st:
@@ -522,8 +549,8 @@ def nvfp4_dequantize(packed: torch.Tensor, sf: torch.Tensor, gsf: torch.Tensor, 
                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """NVFP4 -> bf16: packed uint8 [rows, K/2] + 128x4 scales + device gsf -> bf16 [rows, K]."""
     rows = packed.shape[0]
-    gsf = _scalar(gsf, packed.device, "gsf")
-    y = torch.empty(rows, K, dtype=torch.bfloat16, device=packed.device) if out is None else out
+    gsf = _scalar(gsf, packed.device, "gsf", stream)
+    y = _empty(stream, torch.bfloat16, packed.device, rows, K) if out is None else out
     _check("nvfp4_dequantize", lib().nvfp4_dequantize(_ptr(packed), _ptr(sf), _ptr(gsf), rows, K,
                                                       _ptr(y), _stream(stream)))
     return y
@@ -548,8 +575,8 @@ def nvfp4_linear_fixed_scratch(x: torch.Tensor, w_packed: torch.Tensor, w_sf: to
     for t, name in ((gsf_w, "gsf_w"), (gsf_x, "gsf_x")):
         if t is not None and not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a one-element CUDA float32 tensor")
-    gsf_x = _scalar(gsf_x, x.device, "gsf_x")
-    gsf_w = _scalar(gsf_w, x.device, "gsf_w")
+    gsf_x = _scalar(gsf_x, x.device, "gsf_x", stream)
+    gsf_w = _scalar(gsf_w, x.device, "gsf_w", stream)
     _check("nvfp4_linear_fixed_scratch", lib().nvfp4_linear_fixed_scratch(
         _ptr(x), M, K, _ptr(w_packed), _ptr(w_sf), _ptr(gsf_w), N, _ptr(bias), _ptr(gsf_x),
         int(rotate_group), _ptr(out), _stream(stream)))
