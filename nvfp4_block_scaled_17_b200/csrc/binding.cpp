@@ -259,13 +259,20 @@ void not_over(const EpilogueArgs& e, int64_t M, int64_t N, std::initializer_list
     if (overlap(e.y, 2 * M * cols, e.bias, 2 * N)) throw value_error("out must not overlap bias");
 }
 
-// A linear's workspace holds x's codes while out is written.
-void workspace_apart(const EpilogueArgs& e, int64_t M, int64_t N, const at::Tensor& x, const at::Tensor& ws) {
+// A linear's workspace receives x's codes before the product reads its operands, and holds
+// them while out is written.
+void workspace_apart(const EpilogueArgs& e, int64_t M, int64_t N, const at::Tensor& x, const at::Tensor& ws,
+                     std::initializer_list<Named> operands) {
     const int64_t cols = (e.act & NVFP4_ACT_GATED) ? N / 2 : N;
-    if (overlap(ws.data_ptr(), ws.numel(), x.data_ptr(), 2 * x.numel()))
-        throw value_error("workspace must not overlap x");
-    if (overlap(ws.data_ptr(), ws.numel(), e.residual, 2 * M * cols))
-        throw value_error("workspace must not overlap residual");
+    const void* p = ws.data_ptr();
+    const auto apart = [&](const Named& o) {
+        if (overlap(p, ws.numel(), o.p, o.bytes))
+            throw value_error(std::string("workspace must not overlap ") + o.name);
+    };
+    for (const Named& o : operands) apart(o);
+    apart({"x", x.data_ptr(), 2 * x.numel()});
+    apart({"bias", e.bias, 2 * N});
+    apart({"residual", e.residual, 2 * M * cols});
 }
 
 // (a, sa, b, sb, bias, activation, residual, out, stream)
@@ -324,7 +331,7 @@ PyObject* py_int8_linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
         const at::Tensor* ws = tensor(v[6], "workspace");
         void* pws = need_bytes(ws, "workspace", 0, x);
         not_over(e, M, N, {{"wq", wq, N * K}, {"sw", sw, 4 * N}, {"workspace", pws, ws->numel()}});
-        workspace_apart(e, M, N, x, *ws);
+        workspace_apart(e, M, N, x, *ws, {{"wq", wq, N * K}, {"sw", sw, 4 * N}});
         on_current_device(x, "x");
         if (M == 0 || N == 0) return NVFP4_OK;
         return entries.int8_linear(x.data_ptr(), M, K, static_cast<int8_t*>(wq), static_cast<float*>(sw), N,
@@ -350,7 +357,7 @@ PyObject* py_nvfp4_linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
         const at::Tensor* ws = tensor(v[11], "workspace");
         void* pws = need_bytes(ws, "workspace", 0, x);
         not_over(e, M, N, {{"w_packed", w, N * (K / 2)}, {"w_sf", sf, sf_bytes}, {"workspace", pws, ws->numel()}});
-        workspace_apart(e, M, N, x, *ws);
+        workspace_apart(e, M, N, x, *ws, {{"w_packed", w, N * (K / 2)}, {"w_sf", sf, sf_bytes}});
         const int group = (int)integer(v[8], "rotate_group");
         on_current_device(x, "x");
         if (M == 0 || N == 0) return NVFP4_OK;
