@@ -195,6 +195,26 @@ void codes_apart(const NormArgs& a, const Named& codes, const Named& scales) {
         throw value_error(std::string(scales.name) + " must not overlap the other tensors");
 }
 
+// The device scalars: the scales that are read stay out of the outputs' bytes, alpha_out out of
+// every other tensor's.
+void scalars_apart(const NormArgs& a, const Named& codes, const Named& scales, const void* gsf,
+                   const void* gsf_w, const void* alpha) {
+    const int64_t bytes = 2 * a.R * a.K;
+    const Named outputs[] = {{"residual_out", a.h, bytes}, {"norm_out", a.n, bytes}, codes, scales};
+    const Named inputs[] = {{"x", a.px, bytes}, {"residual", a.residual, bytes},
+                            {"weight", a.weight, 2 * a.K}, {"gsf", gsf, 4}, {"gsf_w", gsf_w, 4}};
+    const auto apart = [](const Named& s, const Named& t) {
+        if (overlap(s.p, s.bytes, t.p, t.bytes))
+            throw value_error(std::string(s.name) + " must not overlap " + t.name);
+    };
+    for (const Named& o : outputs) {
+        apart({"gsf", gsf, 4}, o);
+        apart({"gsf_w", gsf_w, 4}, o);
+        apart({"alpha_out", alpha, 4}, o);
+    }
+    for (const Named& i : inputs) apart({"alpha_out", alpha, 4}, i);
+}
+
 // (x, weight, eps, residual, codes, scales, residual_out, norm_out, stream)
 PyObject* py_int8_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     return guarded(n, 9, [&]() -> int {
@@ -218,9 +238,11 @@ PyObject* py_nvfp4_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
         void* packed = need(tensor(v[5], "packed"), "packed", at::kByte, {a.R, a.K / 2}, *a.x);
         const int64_t sf_bytes = (int64_t)entries.scale_bytes(a.R, a.K);
         void* sf = need_bytes(tensor(v[6], "scales"), "scales", sf_bytes, *a.x);
-        codes_apart(a, {"packed", packed, a.R * (a.K / 2)}, {"scales", sf, sf_bytes});
+        const Named codes{"packed", packed, a.R * (a.K / 2)}, scales{"scales", sf, sf_bytes};
+        codes_apart(a, codes, scales);
         void* gsf_w = need_scalar(tensor(v[7], "gsf_w", true), "gsf_w", *a.x);
         void* alpha = need_scalar(tensor(v[8], "alpha_out", true), "alpha_out", *a.x);
+        scalars_apart(a, codes, scales, gsf, gsf_w, alpha);
         const double eps = number(v[2], "eps");
         on_current_device(*a.x, "x");
         if (a.R == 0) return NVFP4_OK;
@@ -309,7 +331,8 @@ PyObject* py_nvfp4_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
         void* sfb = need_bytes(tensor(v[3], "sfb"), "sfb", sfb_bytes, a);
         void* alpha = need_scalar(tensor(v[5], "alpha"), "alpha", a);
         const EpilogueArgs e = epilogue_args(v[6], v[7], v[8], v[9], M, N, a);
-        not_over(e, M, N, {{"a", pa, M * (K / 2)}, {"b", b, N * (K / 2)}, {"sfa", sfa, sfa_bytes}, {"sfb", sfb, sfb_bytes}});
+        not_over(e, M, N, {{"a", pa, M * (K / 2)}, {"b", b, N * (K / 2)}, {"sfa", sfa, sfa_bytes},
+                           {"sfb", sfb, sfb_bytes}, {"alpha", alpha, 4}});
         on_current_device(a, "a");
         if (M == 0 || N == 0) return NVFP4_OK;
         return entries.nvfp4_gemm(static_cast<uint8_t*>(pa), static_cast<uint8_t*>(sfa),
@@ -356,8 +379,10 @@ PyObject* py_nvfp4_linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
         const EpilogueArgs e = epilogue_args(v[6], v[9], v[10], v[12], M, N, x);
         const at::Tensor* ws = tensor(v[11], "workspace");
         void* pws = need_bytes(ws, "workspace", 0, x);
-        not_over(e, M, N, {{"w_packed", w, N * (K / 2)}, {"w_sf", sf, sf_bytes}, {"workspace", pws, ws->numel()}});
-        workspace_apart(e, M, N, x, *ws, {{"w_packed", w, N * (K / 2)}, {"w_sf", sf, sf_bytes}});
+        not_over(e, M, N, {{"w_packed", w, N * (K / 2)}, {"w_sf", sf, sf_bytes}, {"gsf_w", gsf_w, 4},
+                           {"gsf_x", gsf_x, 4}, {"workspace", pws, ws->numel()}});
+        workspace_apart(e, M, N, x, *ws, {{"w_packed", w, N * (K / 2)}, {"w_sf", sf, sf_bytes},
+                                          {"gsf_w", gsf_w, 4}, {"gsf_x", gsf_x, 4}});
         const int group = (int)integer(v[8], "rotate_group");
         on_current_device(x, "x");
         if (M == 0 || N == 0) return NVFP4_OK;
