@@ -114,8 +114,12 @@ def _calls():
         try:
             from . import _binding
         except ImportError as e:
-            raise RuntimeError("the binding's extension module is missing: build it first "
+            raise RuntimeError(f"the binding's extension module cannot be loaded ({e}): build it first "
                                "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        if _binding.built_for_torch != str(torch.__version__):
+            raise RuntimeError("the binding's extension module was built for PyTorch "
+                               f"{_binding.built_for_torch}, this is {torch.__version__}: build it again "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
         _binding.set_entries(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _BOUND))
         _bound = _binding
     return _bound

@@ -57,13 +57,28 @@ def up_to_date() -> bool:
 OBJ_DIR = os.path.join(ROOT, "_build")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING_PATH = os.path.join(PKG, "_binding.so")
+BINDING_STAMP = os.path.join(OBJ_DIR, "binding.stamp")
+
+
+def _environment() -> str:
+    """What the extension module's binary interface depends on besides its sources."""
+    import torch
+    return (f"torch {torch.__version__}, C++11 ABI {int(torch.compiled_with_cxx11_abi())}, "
+            f"python {sys.version.split()[0]}\n")
+
+
+def _binding_up_to_date() -> bool:
+    if not (os.path.exists(BINDING_PATH) and os.path.exists(BINDING_STAMP)):
+        return False
+    newest = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(INCLUDE, "nvfp4.h"), __file__))
+    with open(BINDING_STAMP) as f:
+        return os.path.getmtime(BINDING_PATH) >= newest and f.read() == _environment()
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """The extension module of the Python binding.  It links against PyTorch only: the CUDA
     library's entry points are handed to it by address."""
-    newest = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(INCLUDE, "nvfp4.h"), __file__))
-    if not force and os.path.exists(BINDING_PATH) and os.path.getmtime(BINDING_PATH) >= newest:
+    if not force and _binding_up_to_date():
         return BINDING_PATH
     import sysconfig
 
@@ -75,12 +90,16 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     tmp = BINDING_PATH + f".{os.getpid()}.tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f'-DBUILT_FOR_TORCH="{torch.__version__}"',
            *[a for d in includes for a in ("-isystem", d)], "-o", tmp, BINDING_SRC, "-L", lib,
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING_PATH)
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_environment())
     return BINDING_PATH
 
 
