@@ -324,7 +324,7 @@ NVFP4_API nvfp4_status int8_linear(const void* x_bf16, int64_t M, int64_t K, con
  *   x            : in,  bf16 [rows, K]; K % 16 == 0, K <= 65536
  *   residual     : in,  bf16 [rows, K] or NULL
  *   weight       : in,  bf16 [K] or NULL (ones)
- *   eps          : host value, finite and > 0
+ *   eps          : host value, finite and at least 2^-255 (1.7e-77), so that rstd is finite
  *   residual_out : out, bf16 [rows, K] = h, or NULL; needs a residual; may equal x or
  *                  residual (in place)
  *   norm_out     : out, bf16 [rows, K] = n, or NULL

@@ -547,7 +547,8 @@ nvfp4_status int8_linear_act(const void* x, int64_t M, int64_t K, const int8_t* 
 
 // The arguments that both norm entry points share.
 static nvfp4_status check_norm(const NormInputs& in) {
-    if (!in.x || in.rows < 0 || !(in.eps > 0.0) || !std::isfinite(in.eps) ||
+    // 1 / sqrt(eps) stays below 2^128, so a row of zeros is 0 times a finite rstd
+    if (!in.x || in.rows < 0 || !(in.eps >= 0x1p-255) || !std::isfinite(in.eps) ||
         (in.residual_out && !in.residual))
         return NVFP4_ERR_INVALID_ARG;
     if (in.K <= 0 || in.K % 16 || in.K > kNormMaxK) return NVFP4_ERR_SHAPE;
