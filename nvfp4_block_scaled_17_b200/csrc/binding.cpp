@@ -77,6 +77,11 @@ void* need_bytes(const at::Tensor* t, const char* name, int64_t least, const at:
     return t->data_ptr();
 }
 
+// The address of n row scales; of none there may be one, as int8_quantize_rows returns it.
+void* need_scales(const at::Tensor* t, const char* name, int64_t n, const at::Tensor& like) {
+    return need(t, name, at::kFloat, {n == 0 && t->dim() == 1 && t->size(0) == 1 ? 1 : n}, like);
+}
+
 // The address of a float32 tensor of one element, of whatever shape.
 void* need_scalar(const at::Tensor* t, const char* name, const at::Tensor& like) {
     if (!t) return nullptr;
@@ -304,8 +309,8 @@ PyObject* py_int8_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
         need_2d(a, "a", at::kChar);
         const int64_t M = a.size(0), K = a.size(1), N = b.dim() == 2 ? b.size(0) : 0;
         void* pb = need(&b, "b", at::kChar, {N, K}, a);
-        void* sa = need(tensor(v[1], "sa"), "sa", at::kFloat, {M}, a);
-        void* sb = need(tensor(v[3], "sb"), "sb", at::kFloat, {N}, a);
+        void* sa = need_scales(tensor(v[1], "sa"), "sa", M, a);
+        void* sb = need_scales(tensor(v[3], "sb"), "sb", N, a);
         const EpilogueArgs e = epilogue_args(v[4], v[5], v[6], v[7], M, N, a);
         not_over(e, M, N, {{"a", a.data_ptr(), M * K}, {"b", pb, N * K}, {"sa", sa, 4 * M}, {"sb", sb, 4 * N}});
         on_current_device(a, "a");
@@ -349,7 +354,7 @@ PyObject* py_int8_linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
         need_2d(x, "x", at::kBFloat16);
         const int64_t M = x.size(0), K = x.size(1), N = w.dim() == 2 ? w.size(0) : 0;
         void* wq = need(&w, "wq", at::kChar, {N, K}, x);
-        void* sw = need(tensor(v[2], "sw"), "sw", at::kFloat, {N}, x);
+        void* sw = need_scales(tensor(v[2], "sw"), "sw", N, x);
         const EpilogueArgs e = epilogue_args(v[3], v[4], v[5], v[7], M, N, x);
         const at::Tensor* ws = tensor(v[6], "workspace");
         void* pws = need_bytes(ws, "workspace", 0, x);
