@@ -140,6 +140,12 @@ int64_t integer(PyObject* o, const char* name) {
     return v;
 }
 
+int int32(PyObject* o, const char* name) {
+    const int64_t v = integer(o, name);
+    if (v != (int)v) throw value_error(std::string(name) + " is out of range");
+    return (int)v;
+}
+
 template <typename F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F&& body) {
     try {
@@ -268,7 +274,7 @@ struct EpilogueArgs {
 EpilogueArgs epilogue_args(PyObject* bias, PyObject* act, PyObject* residual, PyObject* y, int64_t M,
                            int64_t N, const at::Tensor& like) {
     EpilogueArgs e;
-    e.act = (int)integer(act, "activation");
+    e.act = int32(act, "activation");
     const int64_t cols = (e.act & NVFP4_ACT_GATED) ? N / 2 : N;
     e.bias = need(tensor(bias, "bias", true), "bias", at::kBFloat16, {N}, like);
     e.y = need(tensor(y, "out"), "out", at::kBFloat16, {M, cols}, like);
@@ -327,7 +333,7 @@ PyObject* py_nvfp4_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
         const int64_t M = integer(v[10], "M"), N = integer(v[11], "N"), K = integer(v[12], "K");
         if (M < 0 || N < 0 || K < 0) return NVFP4_ERR_INVALID_ARG;
         const at::Tensor& a = *tensor(v[0], "a");
-        const int64_t prepared = integer(v[4], "prepared");
+        const int prepared = int32(v[4], "prepared");
         void* pa = need_bytes(&a, "a", M * (K / 2), a);
         const int64_t sfa_bytes = (int64_t)entries.scale_bytes(M, K);
         void* sfa = need_bytes(tensor(v[1], "sfa"), "sfa", sfa_bytes, a);
@@ -341,7 +347,7 @@ PyObject* py_nvfp4_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
         on_current_device(a, "a");
         if (M == 0 || N == 0) return NVFP4_OK;
         return entries.nvfp4_gemm(static_cast<uint8_t*>(pa), static_cast<uint8_t*>(sfa),
-                                  static_cast<uint8_t*>(b), static_cast<uint8_t*>(sfb), (int)prepared,
+                                  static_cast<uint8_t*>(b), static_cast<uint8_t*>(sfb), prepared,
                                   static_cast<float*>(alpha), e.bias, e.act, e.residual, e.y, M, N, K,
                                   stream_of(v[13]));
     });
@@ -375,7 +381,7 @@ PyObject* py_nvfp4_linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
         need_2d(x, "x", at::kBFloat16);
         const int64_t M = x.size(0), K = x.size(1), N = integer(v[5], "N");
         if (N < 0) return NVFP4_ERR_INVALID_ARG;
-        const int64_t prepared = integer(v[3], "prepared");
+        const int prepared = int32(v[3], "prepared");
         void* w = need_bytes(tensor(v[1], "w_packed"), "w_packed", N * (K / 2), x);
         const int64_t sf_bytes = (int64_t)(prepared ? entries.prepared_bytes(N, K) : entries.scale_bytes(N, K));
         void* sf = need_bytes(tensor(v[2], "w_sf"), "w_sf", sf_bytes, x);
@@ -388,11 +394,11 @@ PyObject* py_nvfp4_linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
                            {"gsf_x", gsf_x, 4}, {"workspace", pws, ws->numel()}});
         workspace_apart(e, M, N, x, *ws, {{"w_packed", w, N * (K / 2)}, {"w_sf", sf, sf_bytes},
                                           {"gsf_w", gsf_w, 4}, {"gsf_x", gsf_x, 4}});
-        const int group = (int)integer(v[8], "rotate_group");
+        const int group = int32(v[8], "rotate_group");
         on_current_device(x, "x");
         if (M == 0 || N == 0) return NVFP4_OK;
         return entries.nvfp4_linear(x.data_ptr(), M, K, static_cast<uint8_t*>(w), static_cast<uint8_t*>(sf),
-                                    (int)prepared, static_cast<float*>(gsf_w), N, e.bias,
+                                    prepared, static_cast<float*>(gsf_w), N, e.bias,
                                     static_cast<float*>(gsf_x), group, e.act, e.residual, pws,
                                     (size_t)ws->numel(), e.y, stream_of(v[13]));
     });
