@@ -384,7 +384,8 @@ NVFP4_API nvfp4_status nvfp4_rmsnorm_quantize(const void* x_bf16, const void* re
  *   residual_bf16 : in,  bf16 [M, n_out] or NULL; may equal y (in place), otherwise may not
  *                   overlap it
  *   y_bf16        : out, bf16 [M, n_out]; overlaps no other tensor
- * int8: K <= 131040, so that every sum of code products is exact in 32 bits.
+ * M and N at most 2^31 - 512.  int8: K <= 131040, so that every sum of code products is exact
+ * in 32 bits.
  * Errors: INVALID_ARG (also an unknown activation, sfb_prepared not 0 or 1), SHAPE (also
  * gated with N odd), ALIGN (also residual 16-byte), DEVICE, CUDA.
  */

@@ -34,6 +34,10 @@ bool valid_activation(int act) {
 // |acc| <= 128 * 128 * K stays below 2^31 for K up to here (a multiple of 32).
 constexpr int64_t kInt8MaxK = 131040;
 
+// Rows and columns of the products with an epilogue: their kernels count up to 511 past the
+// last in 32 bits (the rest of a 256-column tile and what a skipped part of one starts at).
+constexpr int64_t kActMaxSize = (int64_t(1) << 31) - 512;
+
 bool gated(int act) { return (act & NVFP4_ACT_GATED) != 0; }
 
 bool valid_group(int g) { return g == 0 || g == 16 || g == 32 || g == 64 || g == 128; }
@@ -441,7 +445,7 @@ nvfp4_status nvfp4_gemm_act(const uint8_t* a, const uint8_t* sfa, const uint8_t*
     if (!a || !sfa || !b || !sfb || !alpha || !y || M < 0 || N < 0 ||
         (sfb_prepared != 0 && sfb_prepared != 1) || !valid_activation(activation))
         return NVFP4_ERR_INVALID_ARG;
-    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
+    if (M > kActMaxSize || N > kActMaxSize) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 64 || K >= (int64_t(1) << 31) || (gated(activation) && N % 2))
         return NVFP4_ERR_SHAPE;
     if (!aligned(a, 16) || !aligned(sfa, 16) || !aligned(b, 16) || !aligned(sfb, 16) ||
@@ -465,7 +469,7 @@ nvfp4_status nvfp4_linear_act(const void* x, int64_t M, int64_t K, const uint8_t
     if (!x || !w_packed || !w_sf || !gsf_w || !y || M < 0 || N < 0 || !valid_group(group) ||
         (w_sf_prepared != 0 && w_sf_prepared != 1) || !valid_activation(activation))
         return NVFP4_ERR_INVALID_ARG;
-    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
+    if (M > kActMaxSize || N > kActMaxSize) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 64 || (group && K % group) || K >= (int64_t(1) << 31) ||
         (gated(activation) && N % 2))
         return NVFP4_ERR_SHAPE;
@@ -500,7 +504,7 @@ nvfp4_status int8_gemm_act(const int8_t* a, const float* sa, const int8_t* b, co
                            int64_t M, int64_t N, int64_t K, void* stream) {
     if (!a || !sa || !b || !sb || !y || M < 0 || N < 0 || !valid_activation(activation))
         return NVFP4_ERR_INVALID_ARG;
-    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
+    if (M > kActMaxSize || N > kActMaxSize) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 32 || K > kInt8MaxK || (gated(activation) && N % 2)) return NVFP4_ERR_SHAPE;
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16) || !aligned(sa, 16) ||
         !aligned(sb, 16) || (bias && !aligned(bias, 16)) || (residual && !aligned(residual, 16)))
@@ -521,7 +525,7 @@ nvfp4_status int8_linear_act(const void* x, int64_t M, int64_t K, const int8_t* 
                              void* stream) {
     if (!x || !wq || !sw || !y || M < 0 || N < 0 || !valid_activation(activation))
         return NVFP4_ERR_INVALID_ARG;
-    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
+    if (M > kActMaxSize || N > kActMaxSize) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 32 || K > kInt8MaxK || (gated(activation) && N % 2)) return NVFP4_ERR_SHAPE;
     if (!aligned(x, 16) || !aligned(wq, 16) || !aligned(sw, 16) || !aligned(y, 16) ||
         (bias && !aligned(bias, 16)) || (residual && !aligned(residual, 16)))
