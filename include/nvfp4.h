@@ -34,7 +34,8 @@
  *     aligned, scalar pointers 4-byte aligned.
  *   - Argument checks run on the host before anything is enqueued; on any error
  *     nothing is launched and the status says why.  A zero-size call (rows, M or N
- *     equal to 0) returns NVFP4_OK and launches nothing.
+ *     equal to 0) returns NVFP4_OK and launches nothing; the pointers of its tensors
+ *     without elements may be NULL.
  *   - Device-side waits are bounded; a kernel that gives up records
  *     NVFP4_ERR_TIMEOUT in a per-device status word (see nvfp4_last_device_status)
  *     and returns instead of hanging.

@@ -26,6 +26,9 @@ std::mutex g_mu;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// A tensor of n values that is not given; one of none has no address to give.
+bool missing(const void* p, int64_t n) { return !p && n != 0; }
+
 bool valid_activation(int act) {
     const int base = act & ~NVFP4_ACT_GATED;
     return base >= NVFP4_ACT_NONE && base <= NVFP4_ACT_SILU;
@@ -166,7 +169,8 @@ size_t nvfp4_packed_bytes(int64_t rows, int64_t K) {
 
 nvfp4_status hadamard_rotate(const void* x, void* y, int64_t rows, int64_t K, int group,
                              void* stream) {
-    if (!x || !y || rows < 0 || group == 0 || !valid_group(group)) return NVFP4_ERR_INVALID_ARG;
+    if (missing(x, rows) || missing(y, rows) || rows < 0 || group == 0 || !valid_group(group))
+        return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % group) return NVFP4_ERR_SHAPE;
     if (!aligned(x, 16) || !aligned(y, 16)) return NVFP4_ERR_ALIGN;
     DeviceInfo dev;
@@ -182,7 +186,8 @@ nvfp4_status nvfp4_quantize(const void* x, int64_t rows, int64_t K, int group,
                             const float* gsf_in, float* gsf_out, uint8_t* packed, uint8_t* sf,
                             const float* gsf_w, float* alpha_out, void* workspace,
                             size_t ws_bytes, void* stream) {
-    if (!x || !packed || !sf || rows < 0 || !valid_group(group)) return NVFP4_ERR_INVALID_ARG;
+    if (missing(x, rows) || missing(packed, rows) || missing(sf, rows) || rows < 0 || !valid_group(group))
+        return NVFP4_ERR_INVALID_ARG;
     if (!gsf_in && !gsf_out) return NVFP4_ERR_INVALID_ARG;
     if ((gsf_w == nullptr) != (alpha_out == nullptr)) return NVFP4_ERR_INVALID_ARG;
     if ((gsf_w && !aligned(gsf_w, 4)) || (alpha_out && !aligned(alpha_out, 4)))
@@ -207,7 +212,9 @@ nvfp4_status nvfp4_quantize(const void* x, int64_t rows, int64_t K, int group,
 nvfp4_status nvfp4_gemm(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
                         const uint8_t* sfb, const float* alpha, const void* bias, void* y,
                         int64_t M, int64_t N, int64_t K, void* stream) {
-    if (!a || !sfa || !b || !sfb || !alpha || !y || M < 0 || N < 0) return NVFP4_ERR_INVALID_ARG;
+    if (missing(a, M) || missing(sfa, M) || missing(b, N) || missing(sfb, N) || !alpha ||
+        missing(y, M && N) || M < 0 || N < 0)
+        return NVFP4_ERR_INVALID_ARG;
     if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 64 || K >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
     if (!aligned(a, 16) || !aligned(sfa, 16) || !aligned(b, 16) || !aligned(sfb, 16) ||
@@ -223,7 +230,8 @@ nvfp4_status nvfp4_gemm(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
 nvfp4_status nvfp4_gemm_prepared(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
                                  const uint8_t* sfb_prepared, const float* alpha, const void* bias,
                                  void* y, int64_t M, int64_t N, int64_t K, void* stream) {
-    if (!a || !sfa || !b || !sfb_prepared || !alpha || !y || M < 0 || N < 0)
+    if (missing(a, M) || missing(sfa, M) || missing(b, N) || missing(sfb_prepared, N) || !alpha ||
+        missing(y, M && N) || M < 0 || N < 0)
         return NVFP4_ERR_INVALID_ARG;
     if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 64 || K >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
@@ -245,7 +253,8 @@ size_t nvfp4_prepared_scale_bytes(int64_t N, int64_t K) {
 
 nvfp4_status nvfp4_prepare_weight_scales(const uint8_t* sf, int64_t N, int64_t K, uint8_t* out,
                                          void* stream) {
-    if (!sf || !out || N < 0 || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
+    if (missing(sf, N) || missing(out, N) || N < 0 || N >= (int64_t(1) << 31))
+        return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 64 || K >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
     if (!aligned(sf, 16) || !aligned(out, 16)) return NVFP4_ERR_ALIGN;
     DeviceInfo dev;
@@ -257,7 +266,8 @@ nvfp4_status nvfp4_prepare_weight_scales(const uint8_t* sf, int64_t N, int64_t K
 
 nvfp4_status nvfp4_dequantize(const uint8_t* packed, const uint8_t* sf, const float* gsf,
                               int64_t rows, int64_t K, void* y, void* stream) {
-    if (!packed || !sf || !gsf || !y || rows < 0) return NVFP4_ERR_INVALID_ARG;
+    if (missing(packed, rows) || missing(sf, rows) || !gsf || missing(y, rows) || rows < 0)
+        return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 16) return NVFP4_ERR_SHAPE;
     if (!aligned(packed, 16) || !aligned(sf, 16) || !aligned(y, 16) || !aligned(gsf, 4))
         return NVFP4_ERR_ALIGN;
@@ -272,8 +282,8 @@ nvfp4_status nvfp4_gemm_quantize_out(const uint8_t* a, const uint8_t* sfa, const
                                      const uint8_t* sfb, const float* alpha, const void* bias,
                                      const float* gsf_out, uint8_t* out_packed, uint8_t* out_sf,
                                      int64_t M, int64_t N, int64_t K, void* stream) {
-    if (!a || !sfa || !b || !sfb || !alpha || !gsf_out || !out_packed || !out_sf || M < 0 ||
-        N < 0)
+    if (missing(a, M) || missing(sfa, M) || missing(b, N) || missing(sfb, N) || !alpha ||
+        !gsf_out || missing(out_packed, M && N) || missing(out_sf, M && N) || M < 0 || N < 0)
         return NVFP4_ERR_INVALID_ARG;
     if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 64 || K >= (int64_t(1) << 31) || N % 64) return NVFP4_ERR_SHAPE;
@@ -291,7 +301,8 @@ nvfp4_status nvfp4_gemm_quantize_out(const uint8_t* a, const uint8_t* sfa, const
 
 nvfp4_status int8_quantize_rows(const void* x, int64_t rows, int64_t K, int8_t* q, float* scale,
                                 void* stream) {
-    if (!x || !q || !scale || rows < 0) return NVFP4_ERR_INVALID_ARG;
+    if (missing(x, rows) || missing(q, rows) || missing(scale, rows) || rows < 0)
+        return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 16) return NVFP4_ERR_SHAPE;
     if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return NVFP4_ERR_ALIGN;
     DeviceInfo dev;
@@ -303,7 +314,9 @@ nvfp4_status int8_quantize_rows(const void* x, int64_t rows, int64_t K, int8_t* 
 
 nvfp4_status int8_gemm(const int8_t* a, const float* sa, const int8_t* b, const float* sb,
                        const void* bias, void* y, int64_t M, int64_t N, int64_t K, void* stream) {
-    if (!a || !sa || !b || !sb || !y || M < 0 || N < 0) return NVFP4_ERR_INVALID_ARG;
+    if (missing(a, M) || missing(sa, M) || missing(b, N) || missing(sb, N) || missing(y, M && N) ||
+        M < 0 || N < 0)
+        return NVFP4_ERR_INVALID_ARG;
     if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 32 || K >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16) || !aligned(sa, 16) ||
@@ -324,7 +337,8 @@ size_t int8_linear_workspace_bytes(int64_t M, int64_t K) {
 nvfp4_status int8_linear(const void* x, int64_t M, int64_t K, const int8_t* wq, const float* sw,
                          int64_t N, const void* bias, void* workspace, size_t ws_bytes, void* y,
                          void* stream) {
-    if (!x || !wq || !sw || !y || M < 0 || N < 0) return NVFP4_ERR_INVALID_ARG;
+    if (missing(x, M) || missing(wq, N) || missing(sw, N) || missing(y, M && N) || M < 0 || N < 0)
+        return NVFP4_ERR_INVALID_ARG;
     if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 32 || K >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
     if (!aligned(x, 16) || !aligned(wq, 16) || !aligned(sw, 16) || !aligned(y, 16) ||
@@ -357,7 +371,8 @@ static nvfp4_status linear_impl(const void* x, int64_t M, int64_t K, const uint8
                          const uint8_t* w_sf, const float* gsf_w, int64_t N, const void* bias,
                          const float* gsf_x, int group, void* workspace, size_t ws_bytes,
                          void* y, void* stream, bool prepared) {
-    if (!x || !w_packed || !w_sf || !gsf_w || !y || M < 0 || N < 0 || !valid_group(group))
+    if (missing(x, M) || missing(w_packed, N) || missing(w_sf, N) || !gsf_w ||
+        missing(y, M && N) || M < 0 || N < 0 || !valid_group(group))
         return NVFP4_ERR_INVALID_ARG;
     if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 64 || (group && K % group) || K >= (int64_t(1) << 31))
@@ -409,7 +424,8 @@ nvfp4_status nvfp4_linear_fixed_scratch(const void* x, int64_t M, int64_t K,
                                         const uint8_t* w_packed, const uint8_t* w_sf,
                                         const float* gsf_w, int64_t N, const void* bias,
                                         const float* gsf_x, int group, void* y, void* stream) {
-    if (!x || !w_packed || !w_sf || !gsf_w || !y || M < 0 || N < 0 || !valid_group(group))
+    if (missing(x, M) || missing(w_packed, N) || missing(w_sf, N) || !gsf_w ||
+        missing(y, M && N) || M < 0 || N < 0 || !valid_group(group))
         return NVFP4_ERR_INVALID_ARG;
     if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 64 || (group && K % group) || K >= (int64_t(1) << 31))
@@ -442,8 +458,9 @@ nvfp4_status nvfp4_gemm_act(const uint8_t* a, const uint8_t* sfa, const uint8_t*
                             const uint8_t* sfb, int sfb_prepared, const float* alpha,
                             const void* bias, int activation, const void* residual, void* y,
                             int64_t M, int64_t N, int64_t K, void* stream) {
-    if (!a || !sfa || !b || !sfb || !alpha || !y || M < 0 || N < 0 ||
-        (sfb_prepared != 0 && sfb_prepared != 1) || !valid_activation(activation))
+    if (missing(a, M) || missing(sfa, M) || missing(b, N) || missing(sfb, N) || !alpha ||
+        missing(y, M && N) || M < 0 || N < 0 || (sfb_prepared != 0 && sfb_prepared != 1) ||
+        !valid_activation(activation))
         return NVFP4_ERR_INVALID_ARG;
     if (M > kActMaxSize || N > kActMaxSize) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 64 || K >= (int64_t(1) << 31) || (gated(activation) && N % 2))
@@ -466,7 +483,8 @@ nvfp4_status nvfp4_linear_act(const void* x, int64_t M, int64_t K, const uint8_t
                               int64_t N, const void* bias, const float* gsf_x, int group,
                               int activation, const void* residual, void* workspace,
                               size_t ws_bytes, void* y, void* stream) {
-    if (!x || !w_packed || !w_sf || !gsf_w || !y || M < 0 || N < 0 || !valid_group(group) ||
+    if (missing(x, M) || missing(w_packed, N) || missing(w_sf, N) || !gsf_w ||
+        missing(y, M && N) || M < 0 || N < 0 || !valid_group(group) ||
         (w_sf_prepared != 0 && w_sf_prepared != 1) || !valid_activation(activation))
         return NVFP4_ERR_INVALID_ARG;
     if (M > kActMaxSize || N > kActMaxSize) return NVFP4_ERR_INVALID_ARG;
@@ -502,7 +520,8 @@ nvfp4_status nvfp4_linear_act(const void* x, int64_t M, int64_t K, const uint8_t
 nvfp4_status int8_gemm_act(const int8_t* a, const float* sa, const int8_t* b, const float* sb,
                            const void* bias, int activation, const void* residual, void* y,
                            int64_t M, int64_t N, int64_t K, void* stream) {
-    if (!a || !sa || !b || !sb || !y || M < 0 || N < 0 || !valid_activation(activation))
+    if (missing(a, M) || missing(sa, M) || missing(b, N) || missing(sb, N) || missing(y, M && N) ||
+        M < 0 || N < 0 || !valid_activation(activation))
         return NVFP4_ERR_INVALID_ARG;
     if (M > kActMaxSize || N > kActMaxSize) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 32 || K > kInt8MaxK || (gated(activation) && N % 2)) return NVFP4_ERR_SHAPE;
@@ -523,7 +542,8 @@ nvfp4_status int8_linear_act(const void* x, int64_t M, int64_t K, const int8_t* 
                              const float* sw, int64_t N, const void* bias, int activation,
                              const void* residual, void* workspace, size_t ws_bytes, void* y,
                              void* stream) {
-    if (!x || !wq || !sw || !y || M < 0 || N < 0 || !valid_activation(activation))
+    if (missing(x, M) || missing(wq, N) || missing(sw, N) || missing(y, M && N) || M < 0 ||
+        N < 0 || !valid_activation(activation))
         return NVFP4_ERR_INVALID_ARG;
     if (M > kActMaxSize || N > kActMaxSize) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 32 || K > kInt8MaxK || (gated(activation) && N % 2)) return NVFP4_ERR_SHAPE;
@@ -552,7 +572,7 @@ nvfp4_status int8_linear_act(const void* x, int64_t M, int64_t K, const int8_t* 
 // The arguments that both norm entry points share.
 static nvfp4_status check_norm(const NormInputs& in) {
     // 1 / sqrt(eps) stays below 2^128, so a row of zeros is 0 times a finite rstd
-    if (!in.x || in.rows < 0 || !(in.eps >= 0x1p-255) || !std::isfinite(in.eps) ||
+    if (missing(in.x, in.rows) || in.rows < 0 || !(in.eps >= 0x1p-255) || !std::isfinite(in.eps) ||
         (in.residual_out && !in.residual))
         return NVFP4_ERR_INVALID_ARG;
     if (in.K <= 0 || in.K % 16 || in.K > kNormMaxK) return NVFP4_ERR_SHAPE;
@@ -568,7 +588,7 @@ nvfp4_status int8_rmsnorm_quantize(const void* x, const void* residual, const vo
                                    double eps, int64_t rows, int64_t K, int8_t* q, float* scale,
                                    void* residual_out, void* norm_out, void* stream) {
     const NormInputs in{x, residual, weight, eps, rows, K, residual_out, norm_out};
-    if (!q || !scale) return NVFP4_ERR_INVALID_ARG;
+    if (missing(q, rows) || missing(scale, rows)) return NVFP4_ERR_INVALID_ARG;
     nvfp4_status st = check_norm(in);
     if (st != NVFP4_OK) return st;
     if (!aligned(q, 16) || !aligned(scale, 4)) return NVFP4_ERR_ALIGN;
@@ -585,7 +605,7 @@ nvfp4_status nvfp4_rmsnorm_quantize(const void* x, const void* residual, const v
                                     float* alpha_out, void* residual_out, void* norm_out,
                                     void* stream) {
     const NormInputs in{x, residual, weight, eps, rows, K, residual_out, norm_out};
-    if (!gsf || !packed || !sf || (gsf_w == nullptr) != (alpha_out == nullptr))
+    if (!gsf || missing(packed, rows) || missing(sf, rows) || (gsf_w == nullptr) != (alpha_out == nullptr))
         return NVFP4_ERR_INVALID_ARG;
     nvfp4_status st = check_norm(in);
     if (st != NVFP4_OK) return st;
@@ -604,8 +624,8 @@ nvfp4_status nvfp4_debug_gemm_f32(const uint8_t* a, const uint8_t* sfa, const ui
                                   const uint8_t* sfb, int sfb_prepared, const float* alpha,
                                   const void* bias, float* y_f32, int64_t M, int64_t N, int64_t K,
                                   void* stream) {
-    if (!a || !sfa || !b || !sfb || !alpha || !y_f32 || M < 0 || N < 0 ||
-        (sfb_prepared != 0 && sfb_prepared != 1))
+    if (missing(a, M) || missing(sfa, M) || missing(b, N) || missing(sfb, N) || !alpha ||
+        missing(y_f32, M && N) || M < 0 || N < 0 || (sfb_prepared != 0 && sfb_prepared != 1))
         return NVFP4_ERR_INVALID_ARG;
     if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARG;
     if (K <= 0 || K % 64 || K >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
