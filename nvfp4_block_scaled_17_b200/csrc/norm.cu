@@ -311,16 +311,19 @@ nvfp4_status launch_norm(const NormParams& p, int threads, const DeviceInfo& dev
 
 template <bool FP4>
 nvfp4_status dispatch_norm(const NormParams& p, const DeviceInfo& dev, cudaStream_t stream) {
-    // A warp per row as long as a lane has one unit (no block barrier; 32768 x 512 int8 22.5
-    // us against 26.3 with a block per row), then a block per row with one unit per thread:
-    // more units on fewer threads lengthen the chain of a row (1040 values, int8: 777 rows
-    // 5.7 us with a warp of three units a lane, 3.5 with a block of 96 threads; 32768 rows
-    // 89.6 and 65.0).  Above 1024 units a thread takes two or four.
+    // A warp per row as long as a lane has one unit (no block barrier; 32768 x 512 int8 20.4
+    // us against 23.4 with a block per row), then a block per row with one unit per thread:
+    // more units on fewer threads lengthen the chain of a row (1040 values: 777 rows int8 4.1 us
+    // with a warp of three units a lane, 3.1 with a block of 96 threads; 32768 rows int8 50.4
+    // and 57.0, FP4 55.1 and 51.1).  Above 1024 units a thread takes two or four.
     const int U = p.units_padded;
     if (U <= 32) return launch_norm<FP4, 1, false>(p, kNormWarpThreads, dev, stream);
-    // two units a lane as well when there are rows for every warp: 32768 x 1024 FP4 37.6 us,
-    // 39.0 with blocks of 64 threads; 777 x 1024 3.2 and 2.9
-    if (U <= 64 && p.rows >= 4096) return launch_norm<FP4, 2, false>(p, kNormWarpThreads, dev, stream);
+    // Two units a lane as well from 2400 rows on, where blocks go into another round (16 rows a
+    // SM is 2368).  Warps : blocks, us, 528 and 1024 values: int8 2048 rows 3.79 : 3.69 and
+    // 4.01 : 4.00, 2400 rows 5.37 : 5.81 and 5.97 : 6.50, 32768 rows 30.5 : 37.7 and 39.1 :
+    // 40.6; FP4 2368 rows 4.66 : 4.37 and 5.07 : 4.70, 2400 rows 5.41 : 5.45 and 5.97 : 6.25,
+    // 32768 rows 28.2 : 33.7 and 37.4 : 37.8.
+    if (U <= 64 && p.rows >= 2400) return launch_norm<FP4, 2, false>(p, kNormWarpThreads, dev, stream);
     if (U <= 1024) return launch_norm<FP4, 1, true>(p, (U + 31) / 32 * 32, dev, stream);
     if (U <= 2048) return launch_norm<FP4, 2, true>(p, ((U + 1) / 2 + 31) / 32 * 32, dev, stream);
     return launch_norm<FP4, 4, true>(p, ((U + 3) / 4 + 31) / 32 * 32, dev, stream);
