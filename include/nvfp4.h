@@ -403,7 +403,8 @@ NVFP4_API nvfp4_status int8_gemm_act(const int8_t* a, const float* sa, const int
 /*
  * nvfp4_linear_act, int8_linear_act -- nvfp4_linear (nvfp4_linear_prepared with
  * w_sf_prepared = 1) and int8_linear ending in the same epilogue; arguments, workspace and
- * errors otherwise as theirs.  y may be x itself (N = K): x is read before y is written.
+ * errors otherwise as theirs.  y may be x itself (N = K): x is read before y is written.  The
+ * workspace overlaps no tensor of the call.
  */
 NVFP4_API nvfp4_status nvfp4_linear_act(const void* x_bf16, int64_t M, int64_t K,
                                         const uint8_t* w_packed, const uint8_t* w_sf,

@@ -20,7 +20,7 @@
 // graph replay: 32768 x 5120 int8 193 us, 6.08 TB/s (0.93 of the measured copy rate; 215
 // before the arithmetic was packed in pairs and the codes were rounded by an addition, 199
 // with a minimum per value that gives a NaN's code, where one branch per row takes 193);
-// 32768 x 1024 FP4 37.5 us, 5.87 TB/s (0.90); a single row of 5120 2.7 us, of which a launch
+// 32768 x 1024 FP4 37.8 us, 5.83 TB/s (0.89); a single row of 5120 2.7 us, of which a launch
 // alone takes two.  Fetching the next row while the current one is worked on gained nothing:
 // six blocks of 320 threads on an SM cover the latency already.
 #include "common.cuh"
