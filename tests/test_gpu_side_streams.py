@@ -114,3 +114,28 @@ def test_outputs_freed_while_the_current_stream_reads_them(calls, name):
         f(other, side)
         torch.cuda.synchronize()
         assert same(got, want)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_branch_of_a_captured_graph(calls, name):
+    """The stream joins a capture of the current one; outputs are used on the current stream."""
+    f, side, x = calls[name], torch.cuda.Stream(), rows(6)
+    inputs = [rows(7), rows(8)]
+    wants = [parts(f(t, None)) for t in inputs]
+    f(x, side)                                           # the stream's first call, outside
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        first = f(x, side)
+        second = f(x, side)
+        main.wait_stream(side)
+        got = parts(first) + parts(second)
+        del first, second
+    for t, want in list(zip(inputs, wants)) * 2:
+        x.copy_(t)
+        scribble()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(got, want + want)
